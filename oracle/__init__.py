@@ -11,3 +11,5 @@ from .sampler import (  # noqa: F401
 )
 from .replay import ReplayRow, replay, replay_row  # noqa: F401
 from .csr import support_csr  # noqa: F401
+from .verify import Request, verify_captured, verify_drafts, verify_request  # noqa: F401
+from .train import distill_row, replay_grad_row  # noqa: F401

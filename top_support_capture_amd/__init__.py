@@ -1,6 +1,8 @@
 """MI355X-native batched top-k / top-p / min-p sampler with exact support capture.
 
-Python binding of the C-ABI library ``libtsc.so`` (declared in ``include/tsc.h``). This module
+Python binding of the C-ABI library ``libtsc.so`` (declared in ``include/tsc.h``; the verification
+of drafted tokens in ``include/tsc_verify.h`` and ``verify.py``, training over captured supports
+in ``include/tsc_train.h`` and ``train.py``). This module
 only marshals arguments: it checks tensor devices and dtypes, allocates the output tensors with
 PyTorch on the logits' device, and calls ``tsc_sample_with_mask`` on the current HIP stream.
 Every step of the sampling runs in the library's HIP kernels; there is no fallback, and the
@@ -8,6 +10,7 @@ import fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -20,7 +23,10 @@ __all__ = ["sample_with_mask", "prepare", "PreparedSample", "SampleOutput", "wor
            "library", "LIB_PATH",
            "ROW_OK", "ROW_OVERFLOW", "ROW_NO_SUPPORT", "ROW_NONFINITE", "ROW_INVALID_PARAM",
            "ROW_ABORTED", "set_wait_limit", "set_debug_poison",
-           "MAX_PACKED_WIDTH", "TscError"]
+           "MAX_PACKED_WIDTH", "TscError",
+           "verify_drafts", "verify_captured", "VerifyOutput", "Support", "support_of",
+           "MAX_DRAFTS", "distill_topk", "DistillOutput", "distill_topk_grad",
+           "DistillGradOutput", "replay_logprob_backward"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtsc.so")
 
@@ -32,8 +38,8 @@ _lib: Optional[ctypes.CDLL] = None
 
 
 class TscError(RuntimeError):
-    def __init__(self, code: int, name: str):
-        super().__init__(f"tsc_sample_with_mask failed: {name} ({code})")
+    def __init__(self, code: int, name: str, call: str = "tsc_sample_with_mask"):
+        super().__init__(f"{call} failed: {name} ({code})")
         self.code = code
 
 
@@ -70,6 +76,26 @@ def library() -> ctypes.CDLL:
     lib.tsc_set_wait_limit.restype = ctypes.c_uint32
     lib.tsc_set_debug_poison.argtypes = [ctypes.c_int32]
     lib.tsc_set_debug_poison.restype = ctypes.c_int32
+    lib.tsc_verify_drafts.argtypes = ([P, I32, I64, I64, P, I32, I64, I64, I64, I32, I64]
+                                      + [P] * 12 + [SZ, P])
+    lib.tsc_verify_drafts_workspace.argtypes = [I64, I32, I64, I32]
+    lib.tsc_verify_captured.argtypes = ([P, P, P, P, I64, I64, I32] * 2 + [I64, I32] + [P] * 10)
+    distill = [P, I32, I64, I64, I64, P, P, P, P, I32, P]
+    lib.tsc_distill_topk.argtypes = distill + [P, P, P, P, SZ, P]
+    lib.tsc_distill_topk_backward.argtypes = distill + [P, P, P, P]
+    lib.tsc_distill_topk_grad.argtypes = distill + [P, P, P, P, P, SZ, P]
+    lib.tsc_replay_logprob_backward.argtypes = [P, I32, I64, I64, I64, P, P, P, I32, P, P, I64, P,
+                                                P, P, P, P, SZ, P]
+    for f in (lib.tsc_verify_drafts, lib.tsc_verify_captured, lib.tsc_distill_topk,
+              lib.tsc_distill_topk_backward, lib.tsc_distill_topk_grad,
+              lib.tsc_replay_logprob_backward):
+        f.restype = I32
+    lib.tsc_distill_topk_workspace.argtypes = [I64, I64]
+    lib.tsc_distill_topk_grad_workspace.argtypes = [I64, I64]
+    lib.tsc_replay_logprob_backward_workspace.argtypes = [I64]
+    for f in (lib.tsc_verify_drafts_workspace, lib.tsc_distill_topk_workspace,
+              lib.tsc_distill_topk_grad_workspace, lib.tsc_replay_logprob_backward_workspace):
+        f.restype = SZ
     _lib = lib
     return lib
 
@@ -112,6 +138,28 @@ def support_bits_ld(V: int) -> int:
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+def _logits_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return TSC_DTYPE_F32
+    if t.dtype == torch.bfloat16:
+        return TSC_DTYPE_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16")
+
+
+@contextlib.contextmanager
+def _on_device(dev: torch.device, stream: Optional[torch.cuda.Stream]):
+    """``dev`` and ``stream`` (default: its current stream) made current for a launch and the
+    allocations around it; gives the stream's handle."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+    elif dev.index is None or dev.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream(dev).cuda_stream
+    else:
+        with torch.cuda.device(dev):
+            yield torch.cuda.current_stream(dev).cuda_stream
 
 
 def _check(t: torch.Tensor, name: str, dtype, n: int, dev) -> None:
@@ -252,7 +300,17 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
     """Log-probability of ``tokens`` under ``logits`` [N, V] normalized over each row's captured
     support: ``packed_ids`` [N, W] / ``lengths`` [N] (int32, as the sampler writes them), or,
     where ``capture_status`` (int8 [N]) is OVERFLOW, the row of ``support_bits`` (uint8 [N, ld]).
-    ``temperature`` float32 [N] divides the logits first (1 = the plain masked log-softmax)."""
+    ``temperature`` float32 [N] divides the logits first (1 = the plain masked log-softmax).
+
+    Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``);
+    with ``stream`` given, their backward pass runs there too."""
+    if torch.is_grad_enabled() and logits.requires_grad:
+        def call():
+            return replay_logprob(logits.detach(), temperature, packed_ids, lengths, tokens,
+                                  capture_status, support_bits, return_logprobs)
+        with torch.cuda.stream(stream):  # None: the current one
+            return ReplayOutput(*ReplayGradient.apply(call, logits, temperature, packed_ids, lengths,
+                                                      tokens, capture_status, support_bits))
     lib = library()
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [N, V] with unit column stride")
@@ -329,3 +387,9 @@ def csr_to_host(csr: SupportCsr, stream: Optional[torch.cuda.Stream] = None):
     ids = csr.ids[:total].cpu().numpy()
     lps = csr.logprobs[:total].cpu().numpy() if csr.logprobs is not None else None
     return offsets.numpy(), ids, lps
+
+
+from .train import (DistillGradOutput, DistillOutput, ReplayGradient, distill_topk,  # noqa: E402
+                    distill_topk_grad, replay_logprob_backward)
+from .verify import (MAX_DRAFTS, Support, VerifyOutput, support_of, verify_captured,  # noqa: E402
+                     verify_drafts)

@@ -1,4 +1,5 @@
-"""Build the HIP library ``libtsc.so`` in-tree for gfx950 with hipcc.
+"""Build the HIP library ``libtsc.so`` in-tree for gfx950 with hipcc: the sampler's translation
+unit (``csrc/``) and that of the operators around it (``csrc_ops/``), compiled side by side.
 
 ``python -m top_support_capture_amd.build`` (or ``build()``) always recompiles. The library is
 placed next to this file, where the Python binding loads it.
@@ -9,10 +10,12 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "tsc_api.hip")]
+SOURCES = [os.path.join(HERE, "csrc", "tsc_api.hip"),
+           os.path.join(HERE, "csrc_ops", "ops_api.hip")]
 LIB = os.path.join(HERE, "libtsc.so")
 ARCH = os.environ.get("TSC_OFFLOAD_ARCH", "gfx950")
 
@@ -24,22 +27,33 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the HIP library cannot be built")
 
 
-def command(out: str = LIB) -> list:
+def command(source: str, out: str) -> list:
     # Code object v5: loadable by the HIP runtime that PyTorch bundles as well as by /opt/rocm's.
     return [hipcc(), f"--offload-arch={ARCH}", "-mcode-object-version=5", "-O3", "-std=c++17",
-            "-fPIC", "-shared",
+            "-fPIC", "-c",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
-            "-o", out] + SOURCES
+            "-I", os.path.join(HERE, "csrc_ops"), "-o", out, source]
+
+
+def _run(commands: list, verbose: bool) -> None:
+    running = []
+    for cmd in commands:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        running.append((cmd, subprocess.Popen(cmd)))
+    failed = [cmd for cmd, p in running if p.wait() != 0]  # every compiler is waited for
+    if failed:
+        raise RuntimeError("failed: " + " ".join(failed[0]))
 
 
 def build(verbose: bool = True) -> str:
-    tmp = LIB + ".tmp"
-    cmd = command(tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    with tempfile.TemporaryDirectory(prefix="tsc_build_") as work:
+        objects = [os.path.join(work, f"{i}.o") for i in range(len(SOURCES))]
+        _run([command(s, o) for s, o in zip(SOURCES, objects)], verbose)
+        tmp = LIB + ".tmp"
+        _run([[hipcc(), f"--offload-arch={ARCH}", "-shared", "-o", tmp] + objects], verbose)
+        os.replace(tmp, LIB)
     return LIB
 
 

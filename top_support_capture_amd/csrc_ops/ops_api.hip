@@ -1,0 +1,335 @@
+// Host side of the C ABI declared in include/tsc_verify.h and include/tsc_train.h: argument
+// validation and kernel launches on the caller's stream. Nothing here allocates device memory or
+// synchronizes; scratch memory is the caller's workspace.
+#include <hip/hip_runtime.h>
+
+#include <mutex>
+
+#include "replay_grad.h"
+#include "tsc_train.h"
+#include "tsc_verify.h"
+#include "verify.h"
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t{1} << 22;  // one workgroup per row: 2^22 * 512 threads fit a grid
+constexpr int64_t kMaxVocab = INT32_MAX - 16;
+
+bool dtype_ok(int32_t dtype) { return dtype == TSC_DTYPE_F32 || dtype == TSC_DTYPE_BF16; }
+
+bool aligned(const void* p, int32_t dtype) {
+  return reinterpret_cast<uintptr_t>(p) % (dtype == TSC_DTYPE_F32 ? 4 : 2) == 0;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Cut {
+  int32_t n;
+  int64_t len;  // a multiple of `unit`
+};
+
+// `rows` rows of V elements cut into slices: enough slices for `target` workgroups in all, at
+// most kMaxSlices a row, none shorter than `unit` or, unless V asks for it, longer than `most`.
+Cut cut_rows(int64_t rows, int64_t V, int64_t unit, int64_t most, int64_t target) {
+  int64_t n = ceil_div(target, rows > 0 ? rows : 1);
+  if (n < ceil_div(V, most)) n = ceil_div(V, most);
+  if (n > ceil_div(V, unit)) n = ceil_div(V, unit);
+  if (n > tsc::kMaxSlices) n = tsc::kMaxSlices;
+  const int64_t len = ceil_div(ceil_div(V, n), unit) * unit;
+  return {(int32_t)ceil_div(V, len), len};
+}
+
+Cut stats_cut(int64_t rows, int64_t V) { return cut_rows(rows, V, 2048, 32768, 2048); }
+Cut race_cut(int64_t N, int64_t V) { return cut_rows(N, V, 2048, 1 << 30, 1024); }
+
+unsigned grid_of(int64_t items) { return (unsigned)(items < kMaxRows ? items : kMaxRows); }
+
+int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
+
+int32_t launched() { return hipGetLastError() == hipSuccess ? TSC_OK : TSC_ERR_HIP; }
+
+struct VerifyLayout {
+  int64_t parts, best, arrived, bytes;  // offsets, and the whole
+  int32_t rows;
+  Cut stats, race;
+};
+
+VerifyLayout verify_layout(int64_t N, int32_t K, int64_t V, bool has_draft) {
+  VerifyLayout l;
+  l.rows = K + 1 + (has_draft ? K : 0);
+  l.stats = stats_cut(N * l.rows, V);
+  l.race = race_cut(N, V);
+  l.parts = 0;
+  l.best = N * l.rows * l.stats.n * (int64_t)sizeof(tsc::RowPart);
+  l.arrived = l.best + N * l.race.n * (int64_t)sizeof(tsc::RacePart);
+  l.bytes = round16(l.arrived + N * 4);
+  return l;
+}
+
+template <int TD, int DD>
+void launch_verify(const tsc::VerifyArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((tsc::verify_stats_kernel<TD, DD>), dim3(grid_of(a.N * a.rows * a.slices)),
+                     dim3(tsc::kOpThreads), 0, s, a);
+  hipLaunchKernelGGL((tsc::verify_race_kernel<TD, DD>), dim3((unsigned)(a.N * a.shares)),
+                     dim3(tsc::kOpThreads), 0, s, a);
+}
+
+// The dynamic LDS limit of a kernel is a per-device attribute, set once per device.
+constexpr int kMaxDevices = 64;
+
+hipError_t allow_table(size_t bytes) {
+  static std::mutex mu;
+  static bool set[kMaxDevices] = {};
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (set[dev]) return hipSuccess;
+  err = hipFuncSetAttribute(reinterpret_cast<const void*>(&tsc::verify_captured_kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err == hipSuccess) set[dev] = true;
+  return err;
+}
+
+uint32_t table_slots(int32_t W) {  // a power of two, at least twice the entries
+  uint32_t n = 64;
+  while (n < 2u * (uint32_t)W) n <<= 1;
+  return n;
+}
+
+int64_t distill_bytes(int64_t N, int64_t V) {
+  return N * stats_cut(N, V).n * (int64_t)sizeof(tsc::RowPart);
+}
+
+// Checks that the distillation's entry points share; TSC_OK with *empty set when there is no row.
+int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld, int32_t W) {
+  if (!dtype_ok(dtype) || N < 0 || V < 1 || V > kMaxVocab || ld < V || W < 1)
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (N > kMaxRows || W > TSC_MAX_PACKED_WIDTH) return TSC_ERR_UNSUPPORTED;
+  if (N > 0 && (!logits || !aligned(logits, dtype))) return TSC_ERR_INVALID_ARGUMENT;
+  return TSC_OK;
+}
+
+int32_t check_workspace(const void* workspace, size_t have, int64_t need) {
+  if (have < (size_t)need) return TSC_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+    return TSC_ERR_INVALID_ARGUMENT;
+  return TSC_OK;
+}
+
+void launch_distill_loss(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
+  const dim3 grid(grid_of(a.N * a.slices)), rows((unsigned)a.N), block(tsc::kOpThreads);
+  if (dtype == TSC_DTYPE_F32) {
+    hipLaunchKernelGGL(tsc::distill_stats_kernel<TSC_DTYPE_F32>, grid, block, 0, s, a);
+    hipLaunchKernelGGL(tsc::distill_loss_kernel<TSC_DTYPE_F32>, rows, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL(tsc::distill_stats_kernel<TSC_DTYPE_BF16>, grid, block, 0, s, a);
+    hipLaunchKernelGGL(tsc::distill_loss_kernel<TSC_DTYPE_BF16>, rows, block, 0, s, a);
+  }
+}
+
+void launch_distill_grad(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
+  const dim3 grid(grid_of(a.N * ceil_div(a.V, tsc::kTile))), block(tsc::kGradThreads);
+  if (dtype == TSC_DTYPE_F32)
+    hipLaunchKernelGGL(tsc::distill_grad_kernel<TSC_DTYPE_F32>, grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL(tsc::distill_grad_kernel<TSC_DTYPE_BF16>, grid, block, 0, s, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tsc_verify_drafts_workspace(int64_t N, int32_t K, int64_t V, int32_t has_draft) {
+  if (N < 1 || N > kMaxRows || K < 0 || K > TSC_MAX_DRAFTS || V < 1 || V > kMaxVocab) return 0;
+  return (size_t)verify_layout(N, K, V, has_draft != 0).bytes;
+}
+
+int32_t tsc_verify_drafts(const void* target_logits, int32_t target_dtype, int64_t target_stride_n,
+                          int64_t target_stride_k, const void* draft_logits, int32_t draft_dtype,
+                          int64_t draft_stride_n, int64_t draft_stride_k, int64_t N, int32_t K,
+                          int64_t V, const float* temperature, const float* draft_temperature,
+                          const int32_t* draft_tokens, const int32_t* draft_counts,
+                          const float* uniforms, const uint64_t* seeds, const uint64_t* positions,
+                          int32_t* tokens, int32_t* accepted, float* logprobs, int8_t* row_status,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(target_dtype) || (draft_logits && !dtype_ok(draft_dtype)))
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (N < 0 || K < 0 || V < 1 || V > kMaxVocab) return TSC_ERR_INVALID_ARGUMENT;
+  if (N > kMaxRows || K > TSC_MAX_DRAFTS) return TSC_ERR_UNSUPPORTED;
+  if (N == 0) return TSC_OK;
+  if (target_stride_n < 0 || (K > 0 && target_stride_k < 0) || draft_stride_n < 0 || draft_stride_k < 0)
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (!target_logits || !aligned(target_logits, target_dtype) ||
+      (draft_logits && !aligned(draft_logits, draft_dtype)))
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (!temperature || !seeds || !positions || !tokens || !accepted || !logprobs || !row_status ||
+      (K > 0 && (!draft_tokens || !uniforms)))
+    return TSC_ERR_INVALID_ARGUMENT;
+  const VerifyLayout l = verify_layout(N, K, V, draft_logits != nullptr);
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, l.bytes)) return e;
+  char* ws = static_cast<char*>(workspace);
+  const tsc::VerifyArgs a{target_logits, target_stride_n, target_stride_k,
+                          K > 0 ? draft_logits : nullptr, draft_stride_n, draft_stride_k,
+                          target_dtype, draft_dtype, N, V, K, temperature, draft_temperature,
+                          draft_tokens, draft_counts, uniforms, seeds, positions, tokens, accepted,
+                          logprobs, row_status, reinterpret_cast<tsc::RowPart*>(ws + l.parts),
+                          reinterpret_cast<tsc::RacePart*>(ws + l.best),
+                          reinterpret_cast<uint32_t*>(ws + l.arrived), l.rows, l.stats.n, l.race.n,
+                          l.stats.len, l.race.len};
+  (void)hipGetLastError();  // start from a clean error state so a launch error is ours
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int32_t dd = draft_logits ? draft_dtype : target_dtype;
+  if (target_dtype == TSC_DTYPE_F32)
+    dd == TSC_DTYPE_F32 ? launch_verify<TSC_DTYPE_F32, TSC_DTYPE_F32>(a, s)
+                        : launch_verify<TSC_DTYPE_F32, TSC_DTYPE_BF16>(a, s);
+  else
+    dd == TSC_DTYPE_F32 ? launch_verify<TSC_DTYPE_BF16, TSC_DTYPE_F32>(a, s)
+                        : launch_verify<TSC_DTYPE_BF16, TSC_DTYPE_BF16>(a, s);
+  return launched();
+}
+
+int32_t tsc_verify_captured(const int32_t* target_ids, const float* target_logprobs,
+                            const int32_t* target_lengths, const int8_t* target_status,
+                            int64_t target_stride_n, int64_t target_stride_k, int32_t W,
+                            const int32_t* draft_ids, const float* draft_logprobs,
+                            const int32_t* draft_lengths, const int8_t* draft_status,
+                            int64_t draft_stride_n, int64_t draft_stride_k, int32_t draft_W,
+                            int64_t N, int32_t K, const int32_t* draft_tokens,
+                            const int32_t* draft_counts, const float* uniforms,
+                            const uint64_t* seeds, const uint64_t* positions, int32_t* tokens,
+                            int32_t* accepted, float* logprobs, int8_t* row_status, void* stream) {
+  if (N < 0 || K < 0 || W < 1 || (draft_ids && draft_W < 1)) return TSC_ERR_INVALID_ARGUMENT;
+  if (N > kMaxRows || K > TSC_MAX_DRAFTS || W > TSC_MAX_PACKED_WIDTH ||
+      (draft_ids && draft_W > TSC_MAX_PACKED_WIDTH))
+    return TSC_ERR_UNSUPPORTED;
+  if (N == 0) return TSC_OK;
+  if (target_stride_n < 0 || target_stride_k < 0 || draft_stride_n < 0 || draft_stride_k < 0)
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (!target_ids || !target_logprobs || !target_lengths || !seeds || !positions || !tokens ||
+      !accepted || !logprobs || !row_status || (K > 0 && (!draft_tokens || !uniforms)) ||
+      (draft_ids && (!draft_logprobs || !draft_lengths)))
+    return TSC_ERR_INVALID_ARGUMENT;
+  const bool has_draft = draft_ids != nullptr && K > 0;
+  const uint32_t slots = has_draft ? table_slots(draft_W) : 0u;
+  const tsc::CapturedArgs a{
+      {target_ids, target_logprobs, target_lengths, target_status, target_stride_n, target_stride_k, W},
+      {has_draft ? draft_ids : nullptr, draft_logprobs, draft_lengths, draft_status, draft_stride_n,
+       draft_stride_k, draft_W},
+      N, K, draft_tokens, draft_counts, uniforms, seeds, positions, tokens, accepted, logprobs,
+      row_status};
+  (void)hipGetLastError();
+  if (allow_table(table_slots(TSC_MAX_PACKED_WIDTH) * 4) != hipSuccess) return TSC_ERR_HIP;
+  hipLaunchKernelGGL(tsc::verify_captured_kernel, dim3((unsigned)N), dim3(tsc::kCapThreads), slots * 4,
+                     reinterpret_cast<hipStream_t>(stream), a);
+  return launched();
+}
+
+size_t tsc_distill_topk_workspace(int64_t N, int64_t V) {
+  if (N < 1 || N > kMaxRows || V < 1 || V > kMaxVocab) return 0;
+  return (size_t)distill_bytes(N, V);
+}
+
+int32_t tsc_distill_topk(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld,
+                         const float* temperature, const int32_t* teacher_ids,
+                         const float* teacher_values, const int32_t* lengths, int32_t W,
+                         const float* teacher_temperature, float* loss, int8_t* row_status,
+                         float* stats, void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld, W)) return e;
+  if (N == 0) return TSC_OK;
+  if (!temperature || !teacher_ids || !teacher_values || !lengths || !loss || !row_status || !stats)
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, distill_bytes(N, V))) return e;
+  const Cut cut = stats_cut(N, V);
+  const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
+                           teacher_temperature, loss, row_status, stats,
+                           static_cast<tsc::RowPart*>(workspace), cut.n, cut.len, nullptr, nullptr};
+  (void)hipGetLastError();
+  launch_distill_loss(a, dtype, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+int32_t tsc_distill_topk_backward(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                                  int64_t ld, const float* temperature, const int32_t* teacher_ids,
+                                  const float* teacher_values, const int32_t* lengths, int32_t W,
+                                  const float* teacher_temperature, const float* stats,
+                                  const float* grad_loss, void* grad_logits, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld, W)) return e;
+  if (N == 0) return TSC_OK;
+  if (!temperature || !teacher_ids || !teacher_values || !lengths || !stats || !grad_loss ||
+      !grad_logits || !aligned(grad_logits, dtype))
+    return TSC_ERR_INVALID_ARGUMENT;
+  const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
+                           teacher_temperature, nullptr, nullptr, const_cast<float*>(stats), nullptr,
+                           0, 0, grad_loss, grad_logits};
+  (void)hipGetLastError();
+  launch_distill_grad(a, dtype, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+}
+
+int32_t tsc_distill_topk_grad(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld,
+                              const float* temperature, const int32_t* teacher_ids,
+                              const float* teacher_values, const int32_t* lengths, int32_t W,
+                              const float* teacher_temperature, const float* grad_loss, float* loss,
+                              int8_t* row_status, void* grad_logits, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld, W)) return e;
+  if (N == 0) return TSC_OK;
+  if (!temperature || !teacher_ids || !teacher_values || !lengths || !grad_loss || !loss ||
+      !row_status || !grad_logits || !aligned(grad_logits, dtype))
+    return TSC_ERR_INVALID_ARGUMENT;
+  const int64_t parts = distill_bytes(N, V);
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, parts + N * 16)) return e;
+  const Cut cut = stats_cut(N, V);
+  const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
+                           teacher_temperature, loss, row_status,
+                           reinterpret_cast<float*>(static_cast<char*>(workspace) + parts),
+                           static_cast<tsc::RowPart*>(workspace), cut.n, cut.len, grad_loss,
+                           grad_logits};
+  (void)hipGetLastError();
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  launch_distill_loss(a, dtype, s);
+  launch_distill_grad(a, dtype, s);
+  return launched();
+}
+
+size_t tsc_distill_topk_grad_workspace(int64_t N, int64_t V) {
+  if (N < 1 || N > kMaxRows || V < 1 || V > kMaxVocab) return 0;
+  return (size_t)(distill_bytes(N, V) + N * 16);
+}
+
+size_t tsc_replay_logprob_backward_workspace(int64_t N) {
+  return N < 1 || N > kMaxRows ? 0 : (size_t)N * 16;
+}
+
+int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                                    int64_t ld, const float* temperature, const int32_t* packed_ids,
+                                    const int32_t* lengths, int32_t W, const int8_t* capture_status,
+                                    const uint8_t* support_bits, int64_t bits_ld,
+                                    const int32_t* tokens, const float* grad_selected,
+                                    const float* grad_logprobs, void* grad_logits, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld, W)) return e;
+  if (N == 0) return TSC_OK;
+  if (!temperature || !packed_ids || !lengths || !tokens || !grad_logits ||
+      !aligned(grad_logits, dtype) || (support_bits && bits_ld < (V + 7) / 8))
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, N * 16)) return e;
+  const tsc::ReplayGradArgs a{logits, N, V, ld, temperature, packed_ids, lengths, W, capture_status,
+                              support_bits, bits_ld, tokens, grad_selected, grad_logprobs,
+                              grad_logits, static_cast<float*>(workspace)};
+  (void)hipGetLastError();
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const dim3 rows((unsigned)N), tiles(grid_of(N * ceil_div(V, tsc::kTile)));
+  if (dtype == TSC_DTYPE_F32) {
+    hipLaunchKernelGGL(tsc::replay_grad_stats_kernel<TSC_DTYPE_F32>, rows, dim3(tsc::kOpThreads), 0, s, a);
+    hipLaunchKernelGGL(tsc::replay_grad_kernel<TSC_DTYPE_F32>, tiles, dim3(tsc::kGradThreads), 0, s, a);
+  } else {
+    hipLaunchKernelGGL(tsc::replay_grad_stats_kernel<TSC_DTYPE_BF16>, rows, dim3(tsc::kOpThreads), 0, s, a);
+    hipLaunchKernelGGL(tsc::replay_grad_kernel<TSC_DTYPE_BF16>, tiles, dim3(tsc::kGradThreads), 0, s, a);
+  }
+  return launched();
+}
+
+}  // extern "C"
