@@ -25,7 +25,7 @@ extern "C" {
  * teacher_temperature NULL (a prefix of a support is renormalised).
  *
  * logits       [N, V] row-major, row stride ld >= V, float32 or bfloat16 (dtype). Read only.
- * N, V         0 <= N <= 2^22, 1 <= V < 2^31 - 16.
+ * N, V         0 <= N <= 2^21, 1 <= V < 2^31 - 16.
  * temperature  [N] float32, normal positive finite.
  * teacher_ids, teacher_values [N, W] int32 and float32: entries past lengths[n] are not read. Ids
  *              in [0, V); an id that occurs twice counts twice. A value of -inf has probability 0.
@@ -89,17 +89,14 @@ size_t tsc_distill_topk_grad_workspace(int64_t N, int64_t V);
  *              are not read.
  * grad_logits  [N, V] out, contiguous, of the logits' dtype; 0 for a row whose status is not
  *              TSC_ROW_OK in the replay.
- * workspace    at least tsc_replay_logprob_backward_workspace() bytes.
+ * Needs no workspace.
  */
 int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N, int64_t V,
                                     int64_t ld, const float* temperature, const int32_t* packed_ids,
                                     const int32_t* lengths, int32_t W, const int8_t* capture_status,
                                     const uint8_t* support_bits, int64_t bits_ld,
                                     const int32_t* tokens, const float* grad_selected,
-                                    const float* grad_logprobs, void* grad_logits, void* workspace,
-                                    size_t workspace_bytes, void* stream);
-
-size_t tsc_replay_logprob_backward_workspace(int64_t N);
+                                    const float* grad_logprobs, void* grad_logits, void* stream);
 
 #ifdef __cplusplus
 }

@@ -45,7 +45,7 @@ extern "C" {
  *              Row i holds the logits after i accepted drafts. Read only.
  * draft_logits [N, K, V] with its own dtype and strides, or NULL: drafts that come without a
  *              distribution (copied from the prompt, or a greedy drafter's): q is 1 at the draft.
- * N, K, V      requests (0 <= N <= 2^22), drafts per request (0 <= K <= TSC_MAX_DRAFTS),
+ * N, K, V      requests (0 <= N <= 2^21), drafts per request (0 <= K <= TSC_MAX_DRAFTS),
  *              vocabulary size (1 <= V < 2^31 - 16).
  * temperature  [N] float32: 0 = greedy (a draft is accepted iff it is the first index of the
  *              target's maximum, which is also the token emitted otherwise; draft_logits and

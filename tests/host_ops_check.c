@@ -47,10 +47,10 @@ int main(void) {
   expect(verify(2, INT32_MAX, 100, 100, DPTR(void, 20), big) == TSC_ERR_UNSUPPORTED, "K too large");
   expect(verify(2, 2, big, 100, DPTR(void, 20), big) == TSC_ERR_INVALID_ARGUMENT, "V too large");
   expect(verify(2, 2, 100, INT64_MIN, DPTR(void, 20), big) == TSC_ERR_INVALID_ARGUMENT, "stride < 0");
-  expect(verify(1 << 22, 256, INT32_MAX - 16, big, NULL, 0) == TSC_ERR_WORKSPACE, "largest sizes, no workspace");
+  expect(verify(1 << 21, 256, INT32_MAX - 16, big, NULL, 0) == TSC_ERR_WORKSPACE, "largest sizes, no workspace");
   expect(verify(2, 2, 100, 100, NULL, big) == TSC_ERR_INVALID_ARGUMENT, "null workspace");
   expect(verify(0, 0, 1, 0, NULL, 0) == TSC_OK, "no requests");
-  expect(tsc_verify_drafts_workspace(1 << 22, 256, INT32_MAX - 16, 1) > 0, "largest workspace");
+  expect(tsc_verify_drafts_workspace(1 << 21, 256, INT32_MAX - 16, 1) > 0, "largest workspace");
   expect(tsc_verify_drafts_workspace(big, 256, 100, 1) == 0, "workspace of an unsupported size");
   expect(tsc_verify_drafts_workspace(1, 0, 1, 1) > 0, "smallest workspace");
 
@@ -63,12 +63,11 @@ int main(void) {
   expect(distill(big, 100, 100, 16, DPTR(void, 20), big) == TSC_ERR_UNSUPPORTED, "distill N too large");
   expect(distill(2, big, big, 16, DPTR(void, 20), big) == TSC_ERR_INVALID_ARGUMENT, "distill V too large");
   expect(distill(2, 100, INT64_MIN, 16, DPTR(void, 20), big) == TSC_ERR_INVALID_ARGUMENT, "distill ld");
-  expect(distill(1 << 22, INT32_MAX - 16, big, 16, NULL, 0) == TSC_ERR_WORKSPACE, "distill workspace");
+  expect(distill(255, INT32_MAX - 16, big, 16, NULL, 0) == TSC_ERR_WORKSPACE, "distill workspace");
   expect(distill(0, 100, 100, 16, NULL, 0) == TSC_OK, "distill without rows");
-  expect(tsc_distill_topk_workspace(big, 100) == 0 && tsc_distill_topk_grad_workspace(-1, 100) == 0 &&
-             tsc_replay_logprob_backward_workspace(big) == 0,
+  expect(tsc_distill_topk_workspace(big, 100) == 0 && tsc_distill_topk_grad_workspace(-1, 100) == 0,
          "workspaces of unsupported sizes");
-  expect(tsc_distill_topk_grad_workspace(1 << 22, INT32_MAX - 16) > 0, "largest gradient workspace");
+  expect(tsc_distill_topk_grad_workspace(100, INT32_MAX - 16) > 0, "largest gradient workspace");
 
   expect(tsc_distill_topk_backward(DPTR(void, 1), TSC_DTYPE_F32, 2, 100, 100, DPTR(float, 2), DPTR(int32_t, 3),
                                    DPTR(float, 4), DPTR(int32_t, 5), 16, NULL, NULL, DPTR(float, 6),
@@ -80,7 +79,7 @@ int main(void) {
          "misaligned gradient");
   expect(tsc_replay_logprob_backward(DPTR(void, 1), TSC_DTYPE_F32, 2, 100, 100, DPTR(float, 2), DPTR(int32_t, 3),
                                      DPTR(int32_t, 4), 16, NULL, DPTR(uint8_t, 5), INT64_MIN, DPTR(int32_t, 6),
-                                     NULL, NULL, DPTR(void, 7), NULL, 0, NULL) == TSC_ERR_INVALID_ARGUMENT,
+                                     NULL, NULL, DPTR(void, 7), NULL) == TSC_ERR_INVALID_ARGUMENT,
          "replay backward bits_ld");
   printf("host operator checks: %d failure(s)\n", failures);
   return failures;

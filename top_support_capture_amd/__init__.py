@@ -85,16 +85,15 @@ def library() -> ctypes.CDLL:
     lib.tsc_distill_topk_backward.argtypes = distill + [P, P, P, P]
     lib.tsc_distill_topk_grad.argtypes = distill + [P, P, P, P, P, SZ, P]
     lib.tsc_replay_logprob_backward.argtypes = [P, I32, I64, I64, I64, P, P, P, I32, P, P, I64, P,
-                                                P, P, P, P, SZ, P]
+                                                P, P, P, P]
     for f in (lib.tsc_verify_drafts, lib.tsc_verify_captured, lib.tsc_distill_topk,
               lib.tsc_distill_topk_backward, lib.tsc_distill_topk_grad,
               lib.tsc_replay_logprob_backward):
         f.restype = I32
     lib.tsc_distill_topk_workspace.argtypes = [I64, I64]
     lib.tsc_distill_topk_grad_workspace.argtypes = [I64, I64]
-    lib.tsc_replay_logprob_backward_workspace.argtypes = [I64]
     for f in (lib.tsc_verify_drafts_workspace, lib.tsc_distill_topk_workspace,
-              lib.tsc_distill_topk_grad_workspace, lib.tsc_replay_logprob_backward_workspace):
+              lib.tsc_distill_topk_grad_workspace):
         f.restype = SZ
     _lib = lib
     return lib

@@ -3,8 +3,9 @@
 // synchronizes; scratch memory is the caller's workspace.
 #include <hip/hip_runtime.h>
 
-#include <mutex>
+#include <atomic>
 
+#include "distill.h"
 #include "replay_grad.h"
 #include "tsc_train.h"
 #include "tsc_verify.h"
@@ -12,7 +13,7 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = int64_t{1} << 22;  // one workgroup per row: 2^22 * 512 threads fit a grid
+constexpr int64_t kMaxRows = int64_t{1} << 21;  // one workgroup per row: 2^21 * 1024 threads fit a grid
 constexpr int64_t kMaxVocab = INT32_MAX - 16;
 
 bool dtype_ok(int32_t dtype) { return dtype == TSC_DTYPE_F32 || dtype == TSC_DTYPE_BF16; }
@@ -40,6 +41,17 @@ Cut cut_rows(int64_t rows, int64_t V, int64_t unit, int64_t most, int64_t target
 }
 
 Cut stats_cut(int64_t rows, int64_t V) { return cut_rows(rows, V, 2048, 32768, 2048); }
+// The distillation's loss: rows enough for the chip, or short ones, are read by one workgroup each.
+Cut loss_cut(int64_t N, int64_t V) {
+  return N >= 256 || V <= 65536 ? Cut{1, V} : stats_cut(N, V);
+}
+// Gradients: segments of rows, as long as their windows allow unless there are few rows.
+Cut grad_cut(int64_t N, int64_t V) {
+  constexpr int64_t unit = tsc::Window<tsc::kGradThreads>::kSize;
+  int64_t len = ceil_div(ceil_div(V, ceil_div(512, N)), unit) * unit;
+  if (len > tsc::kMaxSegment) len = tsc::kMaxSegment;
+  return {(int32_t)ceil_div(V, len), len};
+}
 Cut race_cut(int64_t N, int64_t V) { return cut_rows(N, V, 2048, 1 << 30, 1024); }
 
 unsigned grid_of(int64_t items) { return (unsigned)(items < kMaxRows ? items : kMaxRows); }
@@ -77,18 +89,17 @@ void launch_verify(const tsc::VerifyArgs& a, hipStream_t s) {
 // The dynamic LDS limit of a kernel is a per-device attribute, set once per device.
 constexpr int kMaxDevices = 64;
 
-hipError_t allow_table(size_t bytes) {
-  static std::mutex mu;
-  static bool set[kMaxDevices] = {};
+// Lets `kernel` have up to `bytes` of dynamic LDS on the current device.
+template <class Kernel>
+hipError_t allow_lds(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
   if (err != hipSuccess) return err;
   if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  if (set[dev]) return hipSuccess;
-  err = hipFuncSetAttribute(reinterpret_cast<const void*>(&tsc::verify_captured_kernel),
+  if ((done.load(std::memory_order_acquire) >> dev) & 1u) return hipSuccess;
+  err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err == hipSuccess) set[dev] = true;
+  if (err == hipSuccess) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   return err;
 }
 
@@ -99,7 +110,8 @@ uint32_t table_slots(int32_t W) {  // a power of two, at least twice the entries
 }
 
 int64_t distill_bytes(int64_t N, int64_t V) {
-  return N * stats_cut(N, V).n * (int64_t)sizeof(tsc::RowPart);
+  const Cut cut = loss_cut(N, V);
+  return cut.n > 1 ? N * cut.n * (int64_t)sizeof(tsc::RowPart) : 0;
 }
 
 // Checks that the distillation's entry points share; TSC_OK with *empty set when there is no row.
@@ -119,23 +131,52 @@ int32_t check_workspace(const void* workspace, size_t have, int64_t need) {
 }
 
 void launch_distill_loss(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
-  const dim3 grid(grid_of(a.N * a.slices)), rows((unsigned)a.N), block(tsc::kOpThreads);
+  const dim3 grid(grid_of(a.N * a.slices)), part(tsc::kOpThreads);
+  const dim3 rows((unsigned)a.N), block(tsc::kLossThreads);
   if (dtype == TSC_DTYPE_F32) {
-    hipLaunchKernelGGL(tsc::distill_stats_kernel<TSC_DTYPE_F32>, grid, block, 0, s, a);
+    if (a.slices > 1) hipLaunchKernelGGL(tsc::distill_stats_kernel<TSC_DTYPE_F32>, grid, part, 0, s, a);
     hipLaunchKernelGGL(tsc::distill_loss_kernel<TSC_DTYPE_F32>, rows, block, 0, s, a);
   } else {
-    hipLaunchKernelGGL(tsc::distill_stats_kernel<TSC_DTYPE_BF16>, grid, block, 0, s, a);
+    if (a.slices > 1) hipLaunchKernelGGL(tsc::distill_stats_kernel<TSC_DTYPE_BF16>, grid, part, 0, s, a);
     hipLaunchKernelGGL(tsc::distill_loss_kernel<TSC_DTYPE_BF16>, rows, block, 0, s, a);
   }
 }
 
-void launch_distill_grad(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
-  const dim3 grid(grid_of(a.N * ceil_div(a.V, tsc::kTile))), block(tsc::kGradThreads);
-  if (dtype == TSC_DTYPE_F32)
-    hipLaunchKernelGGL(tsc::distill_grad_kernel<TSC_DTYPE_F32>, grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL(tsc::distill_grad_kernel<TSC_DTYPE_BF16>, grid, block, 0, s, a);
+// A kernel that writes gradients, with LDS for W entries.
+template <int kThr, class Args>
+hipError_t launch_grad(void (*kernel)(Args), const Args& a, int64_t groups, std::atomic<uint64_t>& allowed,
+                       hipStream_t s) {
+  using Ent = tsc::Entries<kThr>;
+  constexpr size_t most = Ent::bytes(TSC_MAX_PACKED_WIDTH) > Ent::bytes(Ent::kMostForTwo)
+                              ? Ent::bytes(TSC_MAX_PACKED_WIDTH) : Ent::bytes(Ent::kMostForTwo);
+  static_assert(most <= 156 * 1024, "beside the kernels' static LDS");
+  const hipError_t err = allow_lds(kernel, most, allowed);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThr), Ent::bytes(a.W), s, a);
+  return hipGetLastError();
 }
+
+hipError_t launch_distill_grad(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
+  static std::atomic<uint64_t> f32{0}, bf16{0};
+  return dtype == TSC_DTYPE_F32
+             ? launch_grad<tsc::kGradThreads>(&tsc::distill_grad_kernel<TSC_DTYPE_F32>, a, a.N * a.segments, f32, s)
+             : launch_grad<tsc::kGradThreads>(&tsc::distill_grad_kernel<TSC_DTYPE_BF16>, a, a.N * a.segments, bf16, s);
+}
+
+// One workgroup per row for loss and gradient together, when there are rows enough or they are
+// short; one launch instead of two or three. (bf16, W = 2048, of which half is used: 256 rows of
+// 151936 take 42 us against 48 and a launch, 1024 rows 160 against 170; 64 rows 35 against 30.)
+bool fused(int64_t N, int64_t V) { return V <= tsc::kMaxSegment && (N >= 128 || V <= 65536); }
+
+hipError_t launch_distill_fused(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
+  static std::atomic<uint64_t> f32{0}, bf16{0};
+  return dtype == TSC_DTYPE_F32
+             ? launch_grad<tsc::kGradThreads>(&tsc::distill_fused_kernel<TSC_DTYPE_F32>, a, a.N, f32, s)
+             : launch_grad<tsc::kGradThreads>(&tsc::distill_fused_kernel<TSC_DTYPE_BF16>, a, a.N, bf16, s);
+}
+
+// Workspace of loss and gradient in one call: slices' states, and the rows' statistics.
+int64_t distill_grad_bytes(int64_t N, int64_t V) { return distill_bytes(N, V) + N * 16; }
 
 }  // namespace
 
@@ -220,7 +261,9 @@ int32_t tsc_verify_captured(const int32_t* target_ids, const float* target_logpr
       N, K, draft_tokens, draft_counts, uniforms, seeds, positions, tokens, accepted, logprobs,
       row_status};
   (void)hipGetLastError();
-  if (allow_table(table_slots(TSC_MAX_PACKED_WIDTH) * 4) != hipSuccess) return TSC_ERR_HIP;
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_lds(&tsc::verify_captured_kernel, table_slots(TSC_MAX_PACKED_WIDTH) * 4, allowed) != hipSuccess)
+    return TSC_ERR_HIP;
   hipLaunchKernelGGL(tsc::verify_captured_kernel, dim3((unsigned)N), dim3(tsc::kCapThreads), slots * 4,
                      reinterpret_cast<hipStream_t>(stream), a);
   return launched();
@@ -241,10 +284,10 @@ int32_t tsc_distill_topk(const void* logits, int32_t dtype, int64_t N, int64_t V
   if (!temperature || !teacher_ids || !teacher_values || !lengths || !loss || !row_status || !stats)
     return TSC_ERR_INVALID_ARGUMENT;
   if (const int32_t e = check_workspace(workspace, workspace_bytes, distill_bytes(N, V))) return e;
-  const Cut cut = stats_cut(N, V);
+  const Cut cut = loss_cut(N, V);
   const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
                            teacher_temperature, loss, row_status, stats,
-                           static_cast<tsc::RowPart*>(workspace), cut.n, cut.len, nullptr, nullptr};
+                           static_cast<tsc::RowPart*>(workspace), cut.n, cut.len, nullptr, nullptr, 0, 0};
   (void)hipGetLastError();
   launch_distill_loss(a, dtype, reinterpret_cast<hipStream_t>(stream));
   return launched();
@@ -260,12 +303,12 @@ int32_t tsc_distill_topk_backward(const void* logits, int32_t dtype, int64_t N, 
   if (!temperature || !teacher_ids || !teacher_values || !lengths || !stats || !grad_loss ||
       !grad_logits || !aligned(grad_logits, dtype))
     return TSC_ERR_INVALID_ARGUMENT;
+  const Cut cut = grad_cut(N, V);
   const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
                            teacher_temperature, nullptr, nullptr, const_cast<float*>(stats), nullptr,
-                           0, 0, grad_loss, grad_logits};
+                           0, 0, grad_loss, grad_logits, cut.n, cut.len};
   (void)hipGetLastError();
-  launch_distill_grad(a, dtype, reinterpret_cast<hipStream_t>(stream));
-  return launched();
+  return launch_distill_grad(a, dtype, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? TSC_OK : TSC_ERR_HIP;
 }
 
 int32_t tsc_distill_topk_grad(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld,
@@ -279,28 +322,25 @@ int32_t tsc_distill_topk_grad(const void* logits, int32_t dtype, int64_t N, int6
   if (!temperature || !teacher_ids || !teacher_values || !lengths || !grad_loss || !loss ||
       !row_status || !grad_logits || !aligned(grad_logits, dtype))
     return TSC_ERR_INVALID_ARGUMENT;
-  const int64_t parts = distill_bytes(N, V);
-  if (const int32_t e = check_workspace(workspace, workspace_bytes, parts + N * 16)) return e;
-  const Cut cut = stats_cut(N, V);
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, distill_grad_bytes(N, V))) return e;
+  const bool one = fused(N, V);
+  const Cut cut = one ? Cut{1, V} : loss_cut(N, V), seg = grad_cut(N, V);
+  char* stats = static_cast<char*>(workspace) + distill_bytes(N, V);
   const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
-                           teacher_temperature, loss, row_status,
-                           reinterpret_cast<float*>(static_cast<char*>(workspace) + parts),
+                           teacher_temperature, loss, row_status, reinterpret_cast<float*>(stats),
                            static_cast<tsc::RowPart*>(workspace), cut.n, cut.len, grad_loss,
-                           grad_logits};
+                           grad_logits, seg.n, seg.len};
   (void)hipGetLastError();
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (one) return launch_distill_fused(a, dtype, s) == hipSuccess ? TSC_OK : TSC_ERR_HIP;
   launch_distill_loss(a, dtype, s);
-  launch_distill_grad(a, dtype, s);
-  return launched();
+  if (const int32_t e = launched()) return e;
+  return launch_distill_grad(a, dtype, s) == hipSuccess ? TSC_OK : TSC_ERR_HIP;
 }
 
 size_t tsc_distill_topk_grad_workspace(int64_t N, int64_t V) {
   if (N < 1 || N > kMaxRows || V < 1 || V > kMaxVocab) return 0;
-  return (size_t)(distill_bytes(N, V) + N * 16);
-}
-
-size_t tsc_replay_logprob_backward_workspace(int64_t N) {
-  return N < 1 || N > kMaxRows ? 0 : (size_t)N * 16;
+  return (size_t)distill_grad_bytes(N, V);
 }
 
 int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N, int64_t V,
@@ -308,28 +348,24 @@ int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N
                                     const int32_t* lengths, int32_t W, const int8_t* capture_status,
                                     const uint8_t* support_bits, int64_t bits_ld,
                                     const int32_t* tokens, const float* grad_selected,
-                                    const float* grad_logprobs, void* grad_logits, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
+                                    const float* grad_logprobs, void* grad_logits, void* stream) {
   if (const int32_t e = check_rows(logits, dtype, N, V, ld, W)) return e;
   if (N == 0) return TSC_OK;
   if (!temperature || !packed_ids || !lengths || !tokens || !grad_logits ||
       !aligned(grad_logits, dtype) || (support_bits && bits_ld < (V + 7) / 8))
     return TSC_ERR_INVALID_ARGUMENT;
-  if (const int32_t e = check_workspace(workspace, workspace_bytes, N * 16)) return e;
+  const Cut cut = grad_cut(N, V);
   const tsc::ReplayGradArgs a{logits, N, V, ld, temperature, packed_ids, lengths, W, capture_status,
                               support_bits, bits_ld, tokens, grad_selected, grad_logprobs,
-                              grad_logits, static_cast<float*>(workspace)};
+                              grad_logits, cut.n, cut.len};
   (void)hipGetLastError();
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 rows((unsigned)N), tiles(grid_of(N * ceil_div(V, tsc::kTile)));
-  if (dtype == TSC_DTYPE_F32) {
-    hipLaunchKernelGGL(tsc::replay_grad_stats_kernel<TSC_DTYPE_F32>, rows, dim3(tsc::kOpThreads), 0, s, a);
-    hipLaunchKernelGGL(tsc::replay_grad_kernel<TSC_DTYPE_F32>, tiles, dim3(tsc::kGradThreads), 0, s, a);
-  } else {
-    hipLaunchKernelGGL(tsc::replay_grad_stats_kernel<TSC_DTYPE_BF16>, rows, dim3(tsc::kOpThreads), 0, s, a);
-    hipLaunchKernelGGL(tsc::replay_grad_kernel<TSC_DTYPE_BF16>, tiles, dim3(tsc::kGradThreads), 0, s, a);
-  }
-  return launched();
+  static std::atomic<uint64_t> f32{0}, bf16{0};
+  const hipError_t err =
+      dtype == TSC_DTYPE_F32
+          ? launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<TSC_DTYPE_F32>, a, N * cut.n, f32, s)
+          : launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<TSC_DTYPE_BF16>, a, N * cut.n, bf16, s);
+  return err == hipSuccess ? TSC_OK : TSC_ERR_HIP;
 }
 
 }  // extern "C"

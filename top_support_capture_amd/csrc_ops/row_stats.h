@@ -28,9 +28,14 @@ struct Row<TSC_DTYPE_BF16> {
   using Bits = uint16_t;
   struct Chunk {
     u32x4 v;
+    __device__ inline void hide() { asm volatile("" : "+v"(v)); }  // a value the compiler cannot see through
   };
   __device__ static inline Chunk load(const Bits* p) {
     return {*reinterpret_cast<const u32x4_by2*>(p)};
+  }
+  // For rows that are not read again: leaves the caches to others.
+  __device__ static inline Chunk load_once(const Bits* p) {
+    return {__builtin_nontemporal_load(reinterpret_cast<const u32x4_by2*>(p))};
   }
   __device__ static inline void unpack(const Chunk& c, float (&x)[8]) {
 #pragma unroll
@@ -40,7 +45,9 @@ struct Row<TSC_DTYPE_BF16> {
     }
   }
   __device__ static inline float get(const Bits* p) { return __uint_as_float((uint32_t)*p << 16); }
-  // Results are rounded once, to nearest even, from the 32-bit value.
+  // Results are rounded once, to nearest even, from the 32-bit value. Whole chunks are stored
+  // nontemporally: a gradient is not read again soon, and what the caches keep instead (a row that
+  // the loss has read) the gradient's pass reads again.
   __device__ static inline void put(Bits* p, float x) { *p = __builtin_bit_cast(uint16_t, (__bf16)x); }
   __device__ static inline void store(Bits* p, const float (&x)[8]) {
     u32x4 v;
@@ -48,7 +55,7 @@ struct Row<TSC_DTYPE_BF16> {
     for (int i = 0; i < 4; ++i)
       v[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i]) |
              (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * i + 1]) << 16;
-    *reinterpret_cast<u32x4_by2*>(p) = v;
+    __builtin_nontemporal_store((u32x4_by2)v, reinterpret_cast<u32x4_by2*>(p));
   }
 };
 
@@ -57,10 +64,15 @@ struct Row<TSC_DTYPE_F32> {
   using Bits = float;
   struct Chunk {
     u32x4 v[2];
+    __device__ inline void hide() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
   };
   __device__ static inline Chunk load(const Bits* p) {
     const u32x4_by4* q = reinterpret_cast<const u32x4_by4*>(p);
     return {{q[0], q[1]}};
+  }
+  __device__ static inline Chunk load_once(const Bits* p) {
+    const u32x4_by4* q = reinterpret_cast<const u32x4_by4*>(p);
+    return {{__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)}};
   }
   __device__ static inline void unpack(const Chunk& c, float (&x)[8]) {
 #pragma unroll
@@ -73,7 +85,8 @@ struct Row<TSC_DTYPE_F32> {
     u32x4 a, b;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(x[i]), b[i] = __float_as_uint(x[i + 4]);
-    q[0] = a, q[1] = b;
+    __builtin_nontemporal_store((u32x4_by4)a, q);
+    __builtin_nontemporal_store((u32x4_by4)b, q + 1);
   }
 };
 
@@ -134,6 +147,12 @@ __device__ inline float exp2_scaled(float d, Scale c) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(d, c.lo, d * c.hi));
 }
 
+// With c = log2(e) / T in one float32: one operation less, and an error of 2^-24 |d c| from c
+// itself beside the product's rounding. For losses and gradients, which are float32 or less;
+// decisions between probabilities take the Scale.
+__device__ inline float exp2_scaled(float d, float c) { return __builtin_amdgcn_exp2f(d * c); }
+__device__ inline float plain_scale(float T) { return (float)(1.4426950408889634074 / (double)T); }
+
 // State of a slice of a row. `s` is NaN when the slice holds a NaN or a +inf. `at` (greedy rows
 // only, whose s is otherwise 1) is the first index of the maximum.
 struct RowPart {
@@ -146,8 +165,8 @@ struct RowPart {
 struct LseState {
   float m = -__builtin_inff();
   double s = 0.0;
-  template <int N>
-  __device__ inline void add(const float (&x)[N], Scale c) {
+  template <int N, class C>
+  __device__ inline void add(const float (&x)[N], C c) {
     float b = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) b = __builtin_fmaxf(b, x[i]);
@@ -164,42 +183,196 @@ struct LseState {
 };
 
 // s relative to m, relative to M >= m instead (both may be -inf: s is 0 then, or NaN).
-__device__ inline double rescaled(double s, float m, float M, Scale c) {
+template <class C>
+__device__ inline double rescaled(double s, float m, float M, C c) {
   return m == M ? s : s * (double)exp2_scaled(m - M, c);
 }
 
-// The workgroup's state from its threads', the same for every thread.
-template <int kW>
-__device__ inline void block_lse(float& m, double& s, Scale c, float* sh_m, double* sh_s) {
+__device__ inline float wave_max(float v) {
+  return wave_reduce(v, [](float p, float q) { return __builtin_fmaxf(p, q); });
+}
+
+// The workgroup's state from its threads', the same for every thread. kW waves; sh_m and sh_s
+// hold one entry each.
+template <int kW, class C>
+__device__ inline void block_lse(float& m, double& s, C c, float* sh_m, double* sh_s) {
+  static_assert(kW <= 8 || kW == 16, "a loop over the waves, or one row of 16 lanes");
   const uint32_t w = threadIdx.x / kWaveSize, lane = threadIdx.x & (kWaveSize - 1);
-  const float wm = wave_reduce(m, [](float a, float b) { return __builtin_fmaxf(a, b); });
+  const float wm = wave_max(m);
   const double ws = wave_reduce(rescaled(s, m, wm, c), SumOp());
   if (lane == 0) sh_m[w] = wm, sh_s[w] = ws;
   lds_barrier();
-  float M = sh_m[0];
+  if constexpr (kW == 16) {
+    const float om = sh_m[lane & 15];
+    m = row16_reduce(om, [](float p, float q) { return __builtin_fmaxf(p, q); });
+    s = row16_reduce(rescaled(sh_s[lane & 15], om, m, c), SumOp());
+  } else {
+    float M = sh_m[0];
 #pragma unroll
-  for (int i = 1; i < kW; ++i) M = __builtin_fmaxf(M, sh_m[i]);
-  double S = 0.0;
+    for (int i = 1; i < kW; ++i) M = __builtin_fmaxf(M, sh_m[i]);
+    double S = 0.0;
 #pragma unroll
-  for (int i = 0; i < kW; ++i) S += rescaled(sh_s[i], sh_m[i], M, c);
-  m = M, s = S;
+    for (int i = 0; i < kW; ++i) S += rescaled(sh_s[i], sh_m[i], M, c);
+    m = M, s = S;
+  }
+}
+
+// A value over the workgroup under op, the same for every thread; sh holds one entry per wave.
+template <int kW, class T, class Op>
+__device__ inline T block_all(T v, Op op, T* sh) {
+  v = wave_reduce(v, op);
+  lds_barrier();  // sh may still be read by an earlier call
+  if ((threadIdx.x & (kWaveSize - 1)) == 0) sh[threadIdx.x / kWaveSize] = v;
+  lds_barrier();
+  if constexpr (kW == 16) {
+    return row16_reduce(sh[threadIdx.x & 15], op);
+  } else {
+    v = sh[0];
+#pragma unroll
+    for (int i = 1; i < kW; ++i) v = op(v, sh[i]);
+    return v;
+  }
+}
+
+// ---- Writing a row with a few scattered entries --------------------------------------------------
+// A gradient row is a stream over the vocabulary plus a term at each of a few thousand ids. The
+// row is written window by window, a chunk per thread: the entries of a window are added up in
+// LDS in float32 and join the stream's chunks there, so that each result is rounded once and
+// stored in whole chunks. (Writing the entries over a finished row instead costs a read and a
+// write of their lines each: for 1000 entries in a row of 151936, more traffic than the row.) The
+// entries are sorted by window first, so that a window looks at its own only.
+constexpr int kMaxWindows = 64;
+
+// kThr * 8 elements. The halves of a thread's chunk lie apart, so that the 16-byte reads of
+// neighbouring lanes neighbour each other.
+template <int kThr>
+struct Window {
+  static constexpr int kSize = kThr * 8;
+  float* f;
+  __device__ inline void clear() const {
+    for (int i = (int)threadIdx.x * 4; i < kSize; i += kThr * 4)
+      *reinterpret_cast<float4*>(f + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  __device__ inline void add(uint32_t at, float v) const {  // at < kSize
+    atomicAdd(f + ((at >> 2) & 1u) * (kThr * 4) + (at >> 3) * 4 + (at & 3u), v);
+  }
+  // Chunk t, left cleared for the window after the next.
+  __device__ inline void take(int t, float (&d)[8]) const {
+    float4* p = reinterpret_cast<float4*>(f + t * 4);
+    const float4 a = p[0], b = p[kThr];
+    d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w;
+    d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+    uint32_t any = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) any |= __float_as_uint(d[e]);
+    if (any != 0u) p[0] = p[kThr] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+};
+
+// LDS of a workgroup that writes such rows: two windows, which take turns so that one barrier
+// separates a window's entries from its chunks, and the entries; one window alone where with two
+// the space for the entries would keep a second workgroup off the CU.
+template <int kThr>
+struct Entries {
+  static constexpr int kSize = Window<kThr>::kSize;
+  static constexpr int64_t kFixed = (2 * kMaxWindows + 4) * 4;
+  static constexpr int64_t kMostForTwo = (78 * 1024 - kFixed - 2 * kSize * 4) / 6;  // entries
+  bool two;
+  float* window;     // [1 or 2][kSize]
+  float* val;        // [W]
+  uint32_t* start;   // [kMaxWindows + 1]
+  uint32_t* cursor;  // [kMaxWindows]
+  uint16_t* rel;     // [W]
+  __host__ __device__ static constexpr size_t bytes(int64_t W) {
+    return (W <= kMostForTwo ? 2 : 1) * kSize * 4 + W * 4 + kFixed + (W + 1) / 2 * 4;
+  }
+  __device__ inline explicit Entries(void* lds, int32_t W) {
+    two = W <= kMostForTwo;
+    window = reinterpret_cast<float*>(lds);
+    val = window + (two ? 2 : 1) * kSize;
+    start = reinterpret_cast<uint32_t*>(val + W);
+    cursor = start + kMaxWindows + 4;
+    rel = reinterpret_cast<uint16_t*>(cursor + kMaxWindows);
+  }
+  // In this order, with a barrier between any two: begin, count of every entry, offsets, place of
+  // every entry. `at` counts from the segment's first element and is below kMaxWindows * kSize.
+  __device__ inline void begin() const {
+    Window<kThr>{window}.clear();
+    if (two) Window<kThr>{window + kSize}.clear();
+    if (threadIdx.x < kMaxWindows) cursor[threadIdx.x] = 0u;
+  }
+  __device__ inline void count(uint32_t at) const { atomicAdd(&cursor[at / kSize], 1u); }
+  __device__ inline void offsets() const {
+    if (threadIdx.x < kMaxWindows) {  // the first wave
+      const uint32_t n = cursor[threadIdx.x], incl = wave_incl_scan(n, SumOp(), 0u);
+      start[threadIdx.x] = cursor[threadIdx.x] = incl - n;
+      if (threadIdx.x == kMaxWindows - 1) start[kMaxWindows] = incl;
+    }
+  }
+  __device__ inline void place(uint32_t at, float v) const {
+    const uint32_t i = atomicAdd(&cursor[at / kSize], 1u);
+    val[i] = v, rel[i] = (uint16_t)(at % kSize);
+  }
+  __device__ inline Window<kThr> at_window(int k) const { return {window + (two ? (k & 1) * kSize : 0)}; }
+  // Window k's turn: use() takes its chunks; add(k + 1) adds the entries of the next.
+  template <class Add, class Use>
+  __device__ inline void turn(int k, Add add, Use use) const {
+    if (two) add(k + 1);
+    use();
+    lds_barrier();
+    if (!two) {
+      add(k + 1);
+      lds_barrier();
+    }
+  }
+  // The entries of window k (none past the last), each through term(value).
+  template <class Term>
+  __device__ inline void add(int k, Term term) const {
+    if (k >= kMaxWindows) return;
+    const Window<kThr> win = at_window(k);
+    for (uint32_t i = start[k] + threadIdx.x; i < start[k + 1]; i += kThr) win.add(rel[i], term(val[i]));
+  }
+};
+
+// A thread's state of row[lo, hi) in a workgroup of kThr threads. passing(b, e) is called when the
+// workgroup has asked for the elements [b, e): what it reads there is on its way or in the caches.
+struct NoVisit {
+  __device__ inline void operator()(int64_t, int64_t) const {}
+};
+template <int DT, int kThr, class C, class Passing = NoVisit>
+__device__ inline LseState thread_stats(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi, C c,
+                                        Passing passing = Passing()) {
+  constexpr int kU = 4;  // chunks in flight per thread
+  constexpr int64_t kStep = (int64_t)kThr * 8;
+  LseState st;
+  const int64_t first = (int64_t)threadIdx.x * 8;
+  int64_t base = lo;
+  for (; base + kU * kStep <= hi; base += kU * kStep) {
+    typename Row<DT>::Chunk v[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) v[u] = Row<DT>::load(row + base + u * kStep + first);
+    passing(base, base + kU * kStep);
+    float f[kU * 8];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) Row<DT>::unpack(v[u], reinterpret_cast<float(&)[8]>(f[u * 8]));
+    st.add(f, c);
+  }
+  if (base < hi) {
+    passing(base, hi);
+    for (int64_t at = base + first; at < hi; at += kStep) {
+      float x[8];
+      load8<DT>(row, at, hi, x);
+      st.add(x, c);
+    }
+  }
+  return st;
 }
 
 // Statistics of row[lo, hi) into *out (threads of one workgroup of kOpThreads).
-template <int DT>
+template <int DT, class C>
 __device__ inline void slice_stats(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
-                                   Scale c, float* sh_m, double* sh_s, RowPart* out) {
-  constexpr int kU = 4;  // chunks in flight per thread
-  LseState st;
-  for (int64_t at = lo + (int64_t)threadIdx.x * 8; at < hi; at += (int64_t)kOpThreads * 8 * kU) {
-    float x[kU][8];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) load8<DT>(row, at + (int64_t)u * kOpThreads * 8, hi, x[u]);
-    float f[kU * 8];
-#pragma unroll
-    for (int i = 0; i < kU * 8; ++i) f[i] = x[i >> 3][i & 7];
-    st.add(f, c);
-  }
+                                   C c, float* sh_m, double* sh_s, RowPart* out) {
+  LseState st = thread_stats<DT, kOpThreads>(row, lo, hi, c);
   block_lse<kOpWaves>(st.m, st.s, c, sh_m, sh_s);
   if (threadIdx.x == 0) *out = {st.m, 0, st.s};
 }
@@ -220,7 +393,7 @@ __device__ inline void slice_argmax(const typename Row<DT>::Bits* row, int64_t l
       if (x[e] > m) m = x[e], at = (int32_t)(p + e);
     }
   }
-  const float wm = wave_reduce(m, [](float a, float b) { return __builtin_fmaxf(a, b); });
+  const float wm = wave_max(m);
   const int32_t wat = wave_reduce(m == wm ? at : INT32_MAX, MinOp());
   const bool wbad = __ballot(bad) != 0;
   const uint32_t w = threadIdx.x / kWaveSize;
@@ -239,8 +412,9 @@ __device__ inline void slice_argmax(const typename Row<DT>::Bits* row, int64_t l
 }
 
 // A row's state from its slices' (n <= 64, one per lane), the same for every lane.
-__device__ inline RowPart merge_slices(RowPart v, Scale c) {
-  const float M = wave_reduce(v.m, [](float a, float b) { return __builtin_fmaxf(a, b); });
+template <class C>
+__device__ inline RowPart merge_slices(RowPart v, C c) {
+  const float M = wave_max(v.m);
   const int32_t at = wave_reduce(v.m == M ? v.at : INT32_MAX, MinOp());
   return {M, at, wave_reduce(rescaled(v.s, v.m, M, c), SumOp())};
 }

@@ -133,10 +133,6 @@ struct RaceEntry {
   __device__ static inline bool race_near(float p, float w) { return __builtin_fabsf(w) < p * kRaceNear; }
 };
 
-__device__ inline float wave_max(float v) {
-  return wave_reduce(v, [](float p, float q) { return __builtin_fmaxf(p, q); });
-}
-
 // The winner among the workgroup's entries; weight(a, b) is the exact weight.
 template <int kW, class Weight>
 __device__ inline RacePart race_winner(const RaceEntry& e, Weight weight, float* sh_score,

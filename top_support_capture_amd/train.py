@@ -194,13 +194,10 @@ def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
             bits_ld = _packed(support_bits, "support_bits", torch.uint8, N, None, dev)
         with _on_device(dev, stream) as s:
             grad = torch.empty((N, V), dtype=logits.dtype, device=dev)
-            nbytes = lib.tsc_replay_logprob_backward_workspace(N)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             code = lib.tsc_replay_logprob_backward(
                 logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), packed_ids.data_ptr(),
                 lengths.data_ptr(), W, _ptr(capture_status), _ptr(support_bits), bits_ld,
-                tokens.data_ptr(), _ptr(grad_selected), _ptr(grad_logprobs), grad.data_ptr(),
-                ws.data_ptr(), nbytes, s)
+                tokens.data_ptr(), _ptr(grad_selected), _ptr(grad_logprobs), grad.data_ptr(), s)
     _raise(lib, code, "tsc_replay_logprob_backward")
     return grad
 
