@@ -126,7 +126,7 @@ def test_workspace_sizes(lib):
     for N, K, V in [(1, 0, 1), (1, 4, 151936), (64, 4, 151936), (3, 256, 2**31 - 17), (2**21, 2, 100)]:
         a, b = (lib.tsc_verify_drafts_workspace(N, K, V, d) for d in (0, 1))
         assert 0 < a <= b and a % 16 == 0 and b % 16 == 0
-        assert a >= N * (K + 1) * 16 + N * 20  # a state per row, a best entry and a counter
+        assert a >= N * (K + 1) * 16 + N * 12  # a state per row, a winner and a counter
     assert lib.tsc_verify_drafts_workspace(0, 4, 100, 1) == 0
     assert lib.tsc_verify_drafts_workspace(1, 257, 100, 1) == 0
     assert lib.tsc_distill_topk_workspace(-1, 10) == 0

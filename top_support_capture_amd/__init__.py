@@ -10,7 +10,6 @@ import fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -147,18 +146,13 @@ def _logits_dtype(t: torch.Tensor, name: str) -> int:
     raise ValueError(f"{name} must be float32 or bfloat16")
 
 
-@contextlib.contextmanager
-def _on_device(dev: torch.device, stream: Optional[torch.cuda.Stream]):
-    """``dev`` and ``stream`` (default: its current stream) made current for a launch and the
-    allocations around it; gives the stream's handle."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-    elif dev.index is None or dev.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream(dev).cuda_stream
-    else:
-        with torch.cuda.device(dev):
-            yield torch.cuda.current_stream(dev).cuda_stream
+def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], go):
+    """``go(handle)`` with ``dev`` and ``stream`` (default: its current stream) current, for the
+    launch and the allocations around it; the usual case costs no context switch."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return go(torch._C._cuda_getCurrentRawStream(dev.index))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return go(torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _check(t: torch.Tensor, name: str, dtype, n: int, dev) -> None:
@@ -307,9 +301,11 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
         def call():
             return replay_logprob(logits.detach(), temperature, packed_ids, lengths, tokens,
                                   capture_status, support_bits, return_logprobs)
-        with torch.cuda.stream(stream):  # None: the current one
-            return ReplayOutput(*ReplayGradient.apply(call, logits, temperature, packed_ids, lengths,
-                                                      tokens, capture_status, support_bits))
+        args = (call, logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits)
+        if stream is None:
+            return ReplayOutput(*ReplayGradient.apply(*args))
+        with torch.cuda.stream(stream):
+            return ReplayOutput(*ReplayGradient.apply(*args))
     lib = library()
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [N, V] with unit column stride")

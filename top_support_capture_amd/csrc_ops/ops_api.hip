@@ -52,7 +52,7 @@ Cut grad_cut(int64_t N, int64_t V) {
   if (len > tsc::kMaxSegment) len = tsc::kMaxSegment;
   return {(int32_t)ceil_div(V, len), len};
 }
-Cut race_cut(int64_t N, int64_t V) { return cut_rows(N, V, 2048, 1 << 30, 1024); }
+Cut race_cut(int64_t N, int64_t V) { return cut_rows(N, V, 2048, 1 << 30, 512); }
 
 unsigned grid_of(int64_t items) { return (unsigned)(items < kMaxRows ? items : kMaxRows); }
 
@@ -73,7 +73,7 @@ VerifyLayout verify_layout(int64_t N, int32_t K, int64_t V, bool has_draft) {
   l.race = race_cut(N, V);
   l.parts = 0;
   l.best = N * l.rows * l.stats.n * (int64_t)sizeof(tsc::RowPart);
-  l.arrived = l.best + N * l.race.n * (int64_t)sizeof(tsc::RacePart);
+  l.arrived = l.best + N * 8;
   l.bytes = round16(l.arrived + N * 4);
   return l;
 }
@@ -216,7 +216,7 @@ int32_t tsc_verify_drafts(const void* target_logits, int32_t target_dtype, int64
                           target_dtype, draft_dtype, N, V, K, temperature, draft_temperature,
                           draft_tokens, draft_counts, uniforms, seeds, positions, tokens, accepted,
                           logprobs, row_status, reinterpret_cast<tsc::RowPart*>(ws + l.parts),
-                          reinterpret_cast<tsc::RacePart*>(ws + l.best),
+                          reinterpret_cast<uint64_t*>(ws + l.best),
                           reinterpret_cast<uint32_t*>(ws + l.arrived), l.rows, l.stats.n, l.race.n,
                           l.stats.len, l.race.len};
   (void)hipGetLastError();  // start from a clean error state so a launch error is ours

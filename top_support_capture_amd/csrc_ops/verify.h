@@ -36,8 +36,8 @@ struct VerifyArgs {
   int8_t* row_status; // [N]
   // Workspace.
   RowPart* parts;     // [N, rows, slices]
-  struct RacePart* best;  // [N, shares]
-  uint32_t* arrived;  // [N]
+  uint64_t* best;     // [N]: the best share's winner so far (see race_key)
+  uint32_t* arrived;  // [N]: shares that are done
   int32_t rows;       // K + 1 target rows, then K draft rows when there is a draft distribution
   int32_t slices, shares;
   int64_t slice_len, share_len;
@@ -49,6 +49,12 @@ struct RacePart {
   int32_t id;
   int32_t pad;
 };
+
+// A winner as one word that compares as it does: the score in float32, then the lower id. 0 when
+// nothing takes part.
+__device__ inline uint64_t race_key(RacePart b) {
+  return b.score > 0.0 ? (uint64_t)__float_as_uint((float)b.score) << 32 | (0xFFFFFFFFu - (uint32_t)b.id) : 0u;
+}
 
 __device__ inline RacePart better(RacePart a, RacePart b) {
   return b.score > a.score || (b.score == a.score && b.id < a.id) ? b : a;
@@ -65,7 +71,7 @@ __global__ void __launch_bounds__(kOpThreads) verify_stats_kernel(VerifyArgs a) 
   for (int64_t item = blockIdx.x; item < a.N * per; item += gridDim.x) {
     const int64_t n = item / per, rest = item - n * per;
     const int32_t r = (int32_t)(rest / a.slices), sl = (int32_t)(rest - (int64_t)r * a.slices);
-    if (rest == 0 && threadIdx.x == 0) a.arrived[n] = 0u;
+    if (rest == 0 && threadIdx.x == 0) a.arrived[n] = 0u, a.best[n] = 0u;
     const float T = a.temperature[n];
     const bool is_draft = r > a.K;
     const int32_t i = is_draft ? r - a.K - 1 : r;
@@ -73,25 +79,60 @@ __global__ void __launch_bounds__(kOpThreads) verify_stats_kernel(VerifyArgs a) 
     if (i > count - (is_draft ? 1 : 0)) continue;  // uniform over the workgroup, as is all below
     const int64_t lo = sl * a.slice_len, hi = lo + a.slice_len < a.V ? lo + a.slice_len : a.V;
     RowPart* out = a.parts + item;
+    if (T == 0.0f && is_draft) continue;
+    const float Ti = is_draft && a.draft_temperature ? a.draft_temperature[n] : T;
+    const int64_t start = is_draft ? n * a.d_sn + i * a.d_sk : n * a.t_sn + i * a.t_sk;
+    const auto* row = (const typename Row<TD>::Bits*)(is_draft ? a.draft : a.target) + start;
     if (T == 0.0f) {
-      if (is_draft) continue;
-      slice_argmax<TD>((const typename Row<TD>::Bits*)a.target + n * a.t_sn + i * a.t_sk, lo, hi,
-                       sh_m, sh_s, sh_at, out);
-    } else if (!is_draft) {
-      slice_stats<TD>((const typename Row<TD>::Bits*)a.target + n * a.t_sn + i * a.t_sk, lo, hi,
-                      make_scale(T), sh_m, sh_s, out);
+      slice_argmax<TD>(row, lo, hi, sh_m, sh_s, sh_at, out);
+    } else if (TD == DD || !is_draft) {
+      slice_stats<TD>(row, lo, hi, make_scale(Ti), sh_m, sh_s, out);
     } else {
-      const float Td = a.draft_temperature ? a.draft_temperature[n] : T;
-      slice_stats<DD>((const typename Row<DD>::Bits*)a.draft + n * a.d_sn + i * a.d_sk, lo, hi,
-                      make_scale(Td), sh_m, sh_s, out);
+      slice_stats<DD>((const typename Row<DD>::Bits*)a.draft + start, lo, hi, make_scale(Ti), sh_m, sh_s, out);
     }
     lds_barrier();  // the shared states are written again by the next item
   }
 }
 
-// t = 1 - u of a Philox word: u = (2 (word >> 9) + 1) / 2^24, both exact in float32.
+// Philox4x32-10 (Salmon et al., SC'11) of the sampler's race, several counters at once: a round's
+// product and exclusive-ors depend on the last round's, so that independent counters side by side
+// fill the pipeline, and gfx950 takes the exclusive-or of three words in one operation.
+__device__ inline uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
+// Words of the groups of four ids from `group` on, under counter word 1 = `stream`.
+template <int N>
+__device__ inline void race_words(uint32_t group, uint32_t stream, uint64_t seed, uint64_t position,
+                                  uint32_t (&out)[N][4]) {
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    out[i][0] = group + (uint32_t)i, out[i][1] = stream;
+    out[i][2] = (uint32_t)position, out[i][3] = (uint32_t)(position >> 32);
+  }
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint64_t a = (uint64_t)0xD2511F53u * out[i][0], b = (uint64_t)0xCD9E8D57u * out[i][2];
+      out[i][0] = xor3((uint32_t)(b >> 32), out[i][1], k0), out[i][1] = (uint32_t)b;
+      out[i][2] = xor3((uint32_t)(a >> 32), out[i][3], k1), out[i][3] = (uint32_t)a;
+    }
+    k0 += 0x9E3779B9u, k1 += 0xBB67AE85u;
+  }
+}
+
+__device__ inline uint32_t race_word(uint32_t id, uint32_t stream, uint64_t seed, uint64_t position) {
+  uint32_t w[1][4];
+  race_words(id >> 2, stream, seed, position, w);
+  const uint32_t j = id & 3u;
+  return j == 0 ? w[0][0] : j == 1 ? w[0][1] : j == 2 ? w[0][2] : w[0][3];
+}
+
+// t = 1 - u of a Philox word: u = (2 (word >> 9) + 1) / 2^24, all exact in float32.
 __device__ inline float race_t(uint32_t word) {
-  return (float)(0x1000000u - (2u * (word >> 9) + 1u)) * 0x1p-24f;
+  return __builtin_fmaf((float)(word >> 9), -0x1p-23f, 1.0f - 0x1p-24f);
 }
 
 // E = -ln u = -ln(1 - t) to about 1e-6 relative: the series for small t (t^6 / 7 below 2^-26),
@@ -107,30 +148,33 @@ __device__ inline float race_exponential(float t) {
 // theirs again in float64. (Two entries that close within one thread of the many are the
 // float32 score's to order.) float32 holds p and q to about 2e-6, exponents down to -40 rounded.
 // A difference p - q below p / 64 would keep too little of that: such a weight is evaluated in
-// float64 at once, but only if its upper bound, (p - q) + p kRaceSlack, can still win.
+// float64. An entry comes that far only if the upper bound of its weight, (p - q) + p kRaceSlack,
+// can still win, which few entries' do.
 constexpr float kRaceClose = 1e-3f, kRaceSlack = 1e-4f, kRaceNear = 1.0f / 64;
+
+// The filter's probability of a logit: the logarithm of 1 / s is part of the exponent, and one
+// float32 c does (its error is within the margins).
+__device__ inline float weight_of(float x, float m, float c, float minus_lg_s) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(x - m, c, minus_lg_s));
+}
 
 struct RaceEntry {
   float score = 0.0f, t = 0.5f;
   float a = 0.0f, b = 0.0f;  // what the exact weight is computed from
   int32_t id = INT32_MAX;
-  // E >= t: an entry whose w / t is no better than `bound` cannot win, and is spared the rest.
-  __device__ inline void offer(float w, float tt, int32_t i, float a_, float b_, float bound) {
-    if (w > bound * tt) {
-      const float sc = w / race_exponential(tt);
-      if (sc > score || (sc == score && i < id)) score = sc, t = tt, a = a_, b = b_, id = i;
-    }
-  }
-  // The same for a weight p - q of close terms; exact() is its float64 value.
+  // An entry of weight p - q; exact() is the float64 value.
   template <class Exact>
-  __device__ inline void offer_near(float p, float w, float tt, int32_t i, float a_, float b_,
-                                    float bound, Exact exact) {
-    if (race_near(p, w) && w + p * kRaceSlack > bound * tt) {
-      const float we = (float)exact(a_, b_);
-      if (we > 0.0f) offer(we, tt, i, a_, b_, bound);
-    }
+  __device__ inline void offer(float p, float q, int32_t i, float tt, float a_, float b_, Exact exact) {
+    float w = p - q;
+    if (race_near(p, w)) w = (float)exact(a_, b_);
+    const float sc = w * __builtin_amdgcn_rcpf(race_exponential(tt));
+    if (sc > score || (sc == score && i < id)) score = sc, t = tt, a = a_, b = b_, id = i;
   }
   __device__ static inline bool race_near(float p, float w) { return __builtin_fabsf(w) < p * kRaceNear; }
+  // E >= t: an entry whose largest possible w / t is no better than `bound` cannot win.
+  __device__ static inline bool can_win(float p, float w, float tt, float bound) {
+    return __builtin_fmaf(p, kRaceSlack, w) > bound * tt;
+  }
 };
 
 // The winner among the workgroup's entries; weight(a, b) is the exact weight.
@@ -188,14 +232,14 @@ __device__ inline Decision first_stop(const int32_t* code, int32_t count, int32_
 }
 
 template <int TD, int DD>
-__global__ void __launch_bounds__(kOpThreads) verify_race_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a) {
   __shared__ RowPart tp[kMaxDrafts + 1], dp[kMaxDrafts];
   __shared__ int32_t code[kMaxDrafts + 1];
   __shared__ float xt[kMaxDrafts];
   __shared__ int32_t sh_stop;
   __shared__ float sh_score[kOpWaves];
   __shared__ RacePart sh_best[kOpWaves];
-  __shared__ uint32_t sh_last;
+  __shared__ uint64_t sh_key;
   using TB = typename Row<TD>::Bits;
   using DB = typename Row<DD>::Bits;
   const int64_t n = blockIdx.x / a.shares;
@@ -294,7 +338,6 @@ __global__ void __launch_bounds__(kOpThreads) verify_race_kernel(VerifyArgs a) {
   const int32_t drafted = rejected ? a.draft_tokens[n * K + stop] : -1;
   const bool subtract = rejected && has_draft;
   const RowPart d = subtract ? dp[stop] : RowPart{0.0f, 0, 1.0};
-  const float inv_t = (float)(1.0 / t.s), inv_d = (float)(1.0 / d.s);
   const TB* tr = trow + (int64_t)stop * a.t_sk;
   const DB* dr = drow + (int64_t)stop * a.d_sk;
   const uint64_t seed = a.seeds[n], position = a.positions[n] + (uint64_t)stop;
@@ -304,75 +347,105 @@ __global__ void __launch_bounds__(kOpThreads) verify_race_kernel(VerifyArgs a) {
     if (subtract) p -= exp(((double)ye - (double)d.m) / (double)Td) / d.s;
     return p;
   };
+  const float c_t = plain_scale(T), c_d = plain_scale(Td);
+  const float lg_t = -__builtin_amdgcn_logf((float)t.s), lg_d = -__builtin_amdgcn_logf((float)d.s);
   RaceEntry best;
-  float bound = 0.0f;  // the wave's best score so far, less the slack
-  for (int64_t at = lo + (int64_t)tid * 8; at - (int64_t)lane * 8 < hi; at += (int64_t)kOpThreads * 8) {
-    float x[8], y[8] = {}, p[8], wt[8];
-    load8<TD>(tr, at, hi, x);
-    if (subtract) load8<DD>(dr, at, hi, y);
+  float bound = 0.0f;  // the wave's best score so far, less the margin
+  const uint32_t stream = rejected ? 1u : 0u;
+  constexpr int64_t kStep = (int64_t)kOpThreads * 8;
+  const int64_t first = lo + (int64_t)tid * 8;
+  auto race_chunk = [&](int64_t at, const float (&x)[8], const float (&y)[8]) {
+    float p[8], w8[8], most = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      p[e] = exp2_scaled(x[e] - t.m, ct) * inv_t;
-      wt[e] = p[e];
-      if (subtract) wt[e] -= exp2_scaled(y[e] - d.m, cd) * inv_d;
-      if (!subtract && at + e == drafted) p[e] = wt[e] = 0.0f;
+      p[e] = weight_of(x[e], t.m, c_t, lg_t);
+      w8[e] = p[e];
+      if (subtract) w8[e] -= weight_of(y[e], d.m, c_d, lg_d);
+      if (!subtract && at + e == drafted) p[e] = w8[e] = 0.0f;
+      most = __builtin_fmaxf(most, p[e]);
     }
+    // t is at least 2^-24: below that share of the bound no word wins, and none is drawn.
+    if (__ballot(most > bound * 0x1p-24f) == 0) return;
+    uint32_t word[2][4];
+    race_words(((uint32_t)at) >> 2, stream, seed, position, word);
     float tt[8];
-    bool drawn[2];  // wave-uniform
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float most = 0.0f;
+    for (int e = 0; e < 8; ++e) tt[e] = race_t(word[e >> 2][e & 3]);
+    // Few lanes have an entry that can still win; those are computed again, one by one. The first
+    // draws make a bound from each lane's heaviest entry, before all of its entries are open.
+#pragma unroll 1
+    for (int turn = bound == 0.0f ? 0 : 1; turn < 2; ++turn) {
+      uint32_t open = 0;
+      if (turn == 0) {
+        float w = 0.0f;
 #pragma unroll
-      for (int e = 4 * h; e < 4 * h + 4; ++e) most = __builtin_fmaxf(most, wt[e] + p[e] * kRaceSlack);
-      // t is at least 2^-24: below that share of the bound no word wins, and none is drawn.
-      drawn[h] = __ballot(most > bound * 0x1p-24f) != 0;
-      if (!drawn[h]) continue;
-      const uint32_t id0 = (uint32_t)at + 4u * h;
-      const uint4 r = philox4x32_10(
-          make_uint4(id0 >> 2, rejected ? 1u : 0u, (uint32_t)position, (uint32_t)(position >> 32)),
-          (uint32_t)seed, (uint32_t)(seed >> 32));
-      const uint32_t word[4] = {r.x, r.y, r.z, r.w};
+        for (int e = 0; e < 8; ++e)
+          if (w8[e] > w) w = w8[e], open = 1u << e;
+      } else {
 #pragma unroll
-      for (int e = 4 * h; e < 4 * h + 4; ++e) {
-        tt[e] = race_t(word[e & 3]);
-        if (!(subtract && RaceEntry::race_near(p[e], wt[e])))
-          best.offer(wt[e], tt[e], (int32_t)(at + e), x[e], y[e], bound);
+        for (int e = 0; e < 8; ++e) open |= RaceEntry::can_win(p[e], w8[e], tt[e], bound) ? 1u << e : 0u;
       }
+      if (__ballot(open != 0u) == 0) continue;
+      while (open != 0u) {
+        const int64_t id = at + __builtin_ctz(open);
+        open &= open - 1u;
+        const float xe = Row<TD>::get(tr + id), ye = subtract ? Row<DD>::get(dr + id) : 0.0f;
+        best.offer(weight_of(xe, t.m, c_t, lg_t), subtract ? weight_of(ye, d.m, c_d, lg_d) : 0.0f,
+                   (int32_t)id, race_t(race_word((uint32_t)id, stream, seed, position)), xe, ye, exact);
+      }
+      bound = __builtin_fmaxf(bound, wave_max(best.score) * (1.0f - kRaceClose));
     }
-    if (drawn[0] || drawn[1]) bound = wave_max(best.score) * (1.0f - kRaceClose);
-    if (subtract) {
+  };
+  // Whole chunks are asked for kAhead steps before their turn: with few waves to a CU, that many
+  // bytes on the way are what keeps the memory busy.
+  constexpr int kAhead = 3;
+  typename Row<TD>::Chunk vx[kAhead];
+  typename Row<DD>::Chunk vy[kAhead] = {};
+  const int64_t most_at = hi >= lo + 8 ? hi - 8 : -1;  // the last place of a whole chunk
+  auto ask = [&](int j, int64_t at) {
+    if (most_at < 0) return;
+    at = at < most_at ? at : most_at;
+    vx[j] = Row<TD>::load(tr + at);
+    if (subtract) vy[j] = Row<DD>::load(dr + at);
+  };
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (drawn[e >> 2])
-          best.offer_near(p[e], wt[e], tt[e], (int32_t)(at + e), x[e], y[e], bound, exact);
+  for (int j = 0; j < kAhead; ++j) ask(j, first + j * kStep);
+#pragma unroll 1
+  for (int64_t at = first; at - (int64_t)lane * 8 < hi; at += kStep) {
+    float x[8], y[8] = {};
+    if (at + 8 <= hi) {
+      Row<TD>::unpack(vx[0], x);
+      if (subtract) Row<DD>::unpack(vy[0], y);
+    } else {
+      load8<TD>(tr, at, hi, x);
+      if (subtract) load8<DD>(dr, at, hi, y);
     }
+#pragma unroll
+    for (int j = 1; j < kAhead; ++j) vx[j - 1] = vx[j], vy[j - 1] = vy[j];
+    ask(kAhead - 1, at + kAhead * kStep);
+    race_chunk(at, x, y);
   }
   const RacePart won = race_winner<kOpWaves>(best, exact, sh_score, sh_best);
+  // The shares meet in two words of the request. Each thread 0 adds its winner, waits for the word's
+  // old value, and only then counts itself in, so that whoever counts last finds every winner in.
+  // (Releasing and acquiring the whole memory at device scope instead, for plain stores of the
+  // winners, took as long as the race: every workgroup wrote back and invalidated its L2.)
   if (tid == 0) {
-    RacePart* slot = a.best + n * a.shares + share;
-    __hip_atomic_store(&slot->id, won.id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(&slot->score), __builtin_bit_cast(uint64_t, won.score),
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sh_last = __hip_atomic_fetch_add(&a.arrived[n], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-              (uint32_t)a.shares - 1u;
+    const uint64_t before =
+        __hip_atomic_fetch_max(&a.best[n], race_key(won), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    uint32_t one = 1u;
+    asm volatile("" : "+v"(one) : "v"((uint32_t)before), "v"((uint32_t)(before >> 32)));  // needs `before`
+    const uint32_t count = __hip_atomic_fetch_add(&a.arrived[n], one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sh_key = count != (uint32_t)a.shares - 1u
+                 ? ~uint64_t{0}
+                 : __hip_atomic_load(&a.best[n], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   lds_barrier();
-  if (sh_last == 0u) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  RacePart b{0.0, INT32_MAX, 0};
-  if ((int32_t)lane < a.shares) {
-    const RacePart* slot = a.best + n * a.shares + lane;
-    b.id = __hip_atomic_load(&slot->id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    b.score = __builtin_bit_cast(
-        double, __hip_atomic_load(reinterpret_cast<const uint64_t*>(&slot->score), __ATOMIC_RELAXED,
-                                  __HIP_MEMORY_SCOPE_AGENT));
-  }
-  const double top = wave_reduce(b.score, MaxOp());
-  b.id = wave_reduce(b.score == top ? b.id : INT32_MAX, MinOp());
-  b.score = top;
-  // No token with p > q: the two distributions agree within rounding, and the draft is as good
-  // a draw from p as any.
-  finish(b.score > 0.0 ? b.id : drafted);
+  const uint64_t key = sh_key;
+  if (key == ~uint64_t{0}) return;
+  // No token with p > q: the two distributions agree within rounding, and the draft is as good a
+  // draw from p as any.
+  finish(key != 0u ? (int32_t)(0xFFFFFFFFu - (uint32_t)key) : drafted);
 }
 
 // ---- Over captured supports ---------------------------------------------------------------------
@@ -517,7 +590,6 @@ __global__ void __launch_bounds__(kCapThreads) verify_captured_kernel(CapturedAr
     lds_barrier();
   }
   const uint64_t seed = a.seeds[n], position = a.positions[n] + (uint64_t)stop;
-  const uint32_t lo = (uint32_t)position, hi = (uint32_t)(position >> 32);
   auto exact = [](float lp, float lq) -> double { return exp((double)lp) - exp((double)lq); };
   RaceEntry best;
   for (int32_t e = (int32_t)tid; e < t_len; e += kCapThreads) {
@@ -537,18 +609,11 @@ __global__ void __launch_bounds__(kCapThreads) verify_captured_kernel(CapturedAr
     } else if (id == drafted) {
       continue;
     }
-    const float p = exp_fast(lp), wt = p - exp_fast(lq);
-    const bool near = RaceEntry::race_near(p, wt);
-    if (wt > 0.0f || near) {
-      const uint4 r = philox4x32_10(make_uint4((uint32_t)id >> 2, rejected ? 1u : 0u, lo, hi),
-                                    (uint32_t)seed, (uint32_t)(seed >> 32));
-      const uint32_t j = (uint32_t)id & 3u;
-      const float tt = race_t(j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w);
-      const float bound = best.score * (1.0f - kRaceClose);
-      if (near)
-        best.offer_near(p, wt, tt, id, lp, lq, bound, exact);
-      else
-        best.offer(wt, tt, id, lp, lq, bound);
+    const float p = exp_fast(lp), q = exp_fast(lq), wt = p - q;
+    if (wt > 0.0f || RaceEntry::race_near(p, wt)) {
+      const float tt = race_t(race_word((uint32_t)id, rejected ? 1u : 0u, seed, position));
+      if (RaceEntry::can_win(p, wt, tt, best.score * (1.0f - kRaceClose)))
+        best.offer(p, q, id, tt, lp, lq, exact);
     }
   }
   const RacePart won = race_winner<kCapWaves>(best, exact, sh_score, sh_best);

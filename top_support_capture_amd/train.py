@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import TscError, _check, _on_device, _logits_dtype, _ptr, library
+from . import TscError, _check, _launch, _logits_dtype, _ptr, library
 
 __all__ = ["distill_topk", "DistillOutput", "distill_topk_grad", "DistillGradOutput",
            "replay_logprob_backward"]
@@ -44,8 +44,8 @@ def _rows(logits: torch.Tensor):
 
 
 def _packed(t: torch.Tensor, name: str, dtype, N: int, W: Optional[int], dev) -> int:
-    if (t.device != dev or t.dtype != dtype or t.dim() != 2 or t.shape[0] != N
-            or (W is not None and t.shape[1] != W) or not t.is_contiguous()):
+    if (t.dim() != 2 or t.shape != (N, t.shape[1] if W is None else W) or t.dtype != dtype
+            or t.device != dev or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor "
                          f"[{N}, {'W' if W is None else W}] on {dev}")
     return t.shape[1]
@@ -59,10 +59,11 @@ def _distill_args(logits, teacher_ids, teacher_values, lengths, temperature, tea
     _check(temperature, "temperature", torch.float32, N, dev)
     if teacher_temperature is not None:
         _check(teacher_temperature, "teacher_temperature", torch.float32, N, dev)
-    for t, name in ((teacher_values, "teacher_values"), (temperature, "temperature"),
-                    (teacher_temperature, "teacher_temperature")):
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"the distillation has no gradient with respect to {name}: detach it")
+    if torch.is_grad_enabled() and (
+            teacher_values.requires_grad or temperature.requires_grad
+            or (teacher_temperature is not None and teacher_temperature.requires_grad)):
+        raise ValueError("the distillation has no gradient with respect to teacher_values, "
+                         "temperature or teacher_temperature: detach them")
     return (logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), teacher_ids.data_ptr(),
             teacher_values.data_ptr(), lengths.data_ptr(), W, _ptr(teacher_temperature)), dev
 
@@ -73,16 +74,40 @@ def _distill_forward(logits, teacher_ids, teacher_values, lengths, temperature,
     args, dev = _distill_args(logits, teacher_ids, teacher_values, lengths, temperature,
                               teacher_temperature)
     N, V = logits.shape
-    with _on_device(dev, stream) as s:
+    nbytes = lib.tsc_distill_topk_workspace(N, V)
+
+    def go(s):
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         status = torch.empty(N, dtype=torch.int8, device=dev)
         stats = torch.empty((N, 4), dtype=torch.float32, device=dev)
-        nbytes = lib.tsc_distill_topk_workspace(N, V)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         code = lib.tsc_distill_topk(*args, loss.data_ptr(), status.data_ptr(), stats.data_ptr(),
-                                    ws.data_ptr(), nbytes, s)
-    _raise(lib, code, "tsc_distill_topk")
-    return loss, status, stats
+                                    _ptr(ws), nbytes, s)
+        _raise(lib, code, "tsc_distill_topk")
+        return loss, status, stats
+
+    return _launch(dev, stream, go)
+
+
+def _distill_backward(ctx, grad_loss):
+    logits, ids, values, lengths, T, teacher_T, stats = ctx.saved_tensors
+    lib = library()
+    args, dev = _distill_args(logits, ids, values, lengths, T, teacher_T)
+
+    def go(s):
+        g = grad_loss.contiguous()
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        code = lib.tsc_distill_topk_backward(*args, stats.data_ptr(), g.data_ptr(),
+                                             grad.data_ptr(), s)
+        _raise(lib, code, "tsc_distill_topk_backward")
+        return grad
+
+    return (_launch(dev, None, go),) + (None,) * 5
+
+
+# Backward passes run without a graph unless one is asked for (create_graph); the gradient has no
+# gradient of its own then, and says so.
+_distill_backward_once = once_differentiable(_distill_backward)
 
 
 class _Distill(torch.autograd.Function):
@@ -98,20 +123,11 @@ class _Distill(torch.autograd.Function):
         return loss, status
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad_loss, _):
         if grad_loss is None:
             return (None,) * 6
-        logits, ids, values, lengths, T, teacher_T, stats = ctx.saved_tensors
-        lib = library()
-        args, dev = _distill_args(logits, ids, values, lengths, T, teacher_T)
-        with _on_device(dev, None) as s:
-            g = grad_loss.contiguous()
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-            code = lib.tsc_distill_topk_backward(*args, stats.data_ptr(), g.data_ptr(),
-                                                 grad.data_ptr(), s)
-        _raise(lib, code, "tsc_distill_topk_backward")
-        return (grad,) + (None,) * 5
+        go = _distill_backward_once if torch.is_grad_enabled() else _distill_backward
+        return go(ctx, grad_loss)
 
 
 def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values: torch.Tensor,
@@ -151,17 +167,20 @@ def distill_topk_grad(logits: torch.Tensor, teacher_ids: torch.Tensor,
                                   teacher_temperature)
         N, V = logits.shape
         _check(row_weights, "row_weights", torch.float32, N, dev)
-        with _on_device(dev, stream) as s:
+        nbytes = lib.tsc_distill_topk_grad_workspace(N, V)
+
+        def go(s):
             out = DistillGradOutput(torch.empty(N, dtype=torch.float32, device=dev),
                                     torch.empty((N, V), dtype=logits.dtype, device=dev),
                                     torch.empty(N, dtype=torch.int8, device=dev))
-            nbytes = lib.tsc_distill_topk_grad_workspace(N, V)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             code = lib.tsc_distill_topk_grad(*args, row_weights.data_ptr(), out.loss.data_ptr(),
                                              out.row_status.data_ptr(), out.grad_logits.data_ptr(),
                                              ws.data_ptr(), nbytes, s)
-    _raise(lib, code, "tsc_distill_topk_grad")
-    return out
+            _raise(lib, code, "tsc_distill_topk_grad")
+            return out
+
+        return _launch(dev, stream, go)
 
 
 def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
@@ -177,29 +196,43 @@ def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
     length are not read). Rows whose replay status is not ROW_OK have gradient 0. This is the
     call that autograd makes; made directly it needs no graph of torch's."""
     lib = library()
-    with torch.no_grad():
-        dt, N, V, ld, dev = _rows(logits)
-        W = _packed(packed_ids, "packed_ids", torch.int32, N, None, dev)
-        _check(temperature, "temperature", torch.float32, N, dev)
-        _check(lengths, "lengths", torch.int32, N, dev)
-        _check(tokens, "tokens", torch.int32, N, dev)
-        if grad_selected is not None:
-            _check(grad_selected, "grad_selected", torch.float32, N, dev)
-        if grad_logprobs is not None:
-            _packed(grad_logprobs, "grad_logprobs", torch.float32, N, W, dev)
-        if capture_status is not None:
-            _check(capture_status, "capture_status", torch.int8, N, dev)
-        bits_ld = 0
-        if support_bits is not None:
-            bits_ld = _packed(support_bits, "support_bits", torch.uint8, N, None, dev)
-        with _on_device(dev, stream) as s:
-            grad = torch.empty((N, V), dtype=logits.dtype, device=dev)
-            code = lib.tsc_replay_logprob_backward(
-                logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), packed_ids.data_ptr(),
-                lengths.data_ptr(), W, _ptr(capture_status), _ptr(support_bits), bits_ld,
-                tokens.data_ptr(), _ptr(grad_selected), _ptr(grad_logprobs), grad.data_ptr(), s)
-    _raise(lib, code, "tsc_replay_logprob_backward")
-    return grad
+    dt, N, V, ld, dev = _rows(logits)
+    W = _packed(packed_ids, "packed_ids", torch.int32, N, None, dev)
+    _check(temperature, "temperature", torch.float32, N, dev)
+    _check(lengths, "lengths", torch.int32, N, dev)
+    _check(tokens, "tokens", torch.int32, N, dev)
+    if grad_selected is not None:
+        _check(grad_selected, "grad_selected", torch.float32, N, dev)
+    if grad_logprobs is not None:
+        _packed(grad_logprobs, "grad_logprobs", torch.float32, N, W, dev)
+    if capture_status is not None:
+        _check(capture_status, "capture_status", torch.int8, N, dev)
+    bits_ld = 0
+    if support_bits is not None:
+        bits_ld = _packed(support_bits, "support_bits", torch.uint8, N, None, dev)
+
+    def go(s):
+        grad = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        code = lib.tsc_replay_logprob_backward(
+            logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), packed_ids.data_ptr(),
+            lengths.data_ptr(), W, _ptr(capture_status), _ptr(support_bits), bits_ld,
+            tokens.data_ptr(), _ptr(grad_selected), _ptr(grad_logprobs), grad.data_ptr(), s)
+        _raise(lib, code, "tsc_replay_logprob_backward")
+        return grad
+
+    return _launch(dev, stream, go)
+
+
+def _replay_backward(ctx, grad_selected, grad_logprobs):
+    logits, T, ids, lengths, tokens, status, bits = ctx.saved_tensors
+    grad = replay_logprob_backward(
+        logits, T, ids, lengths, tokens,
+        None if grad_selected is None else grad_selected.contiguous(),
+        None if grad_logprobs is None else grad_logprobs.contiguous(), status, bits)
+    return (None, grad) + (None,) * 6
+
+
+_replay_backward_once = once_differentiable(_replay_backward)
 
 
 class ReplayGradient(torch.autograd.Function):
@@ -216,13 +249,8 @@ class ReplayGradient(torch.autograd.Function):
         return out.selected_logprob, out.logprobs, out.row_status
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad_selected, grad_logprobs, _):
         if grad_selected is None and grad_logprobs is None:
             return (None,) * 8
-        logits, T, ids, lengths, tokens, status, bits = ctx.saved_tensors
-        grad = replay_logprob_backward(
-            logits, T, ids, lengths, tokens,
-            None if grad_selected is None else grad_selected.contiguous(),
-            None if grad_logprobs is None else grad_logprobs.contiguous(), status, bits)
-        return (None, grad) + (None,) * 6
+        go = _replay_backward_once if torch.is_grad_enabled() else _replay_backward
+        return go(ctx, grad_selected, grad_logprobs)

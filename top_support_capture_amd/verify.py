@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import SampleOutput, TscError, _check, _on_device, _logits_dtype, _ptr, library
+from . import SampleOutput, TscError, _check, _launch, _logits_dtype, _ptr, library
 
 __all__ = ["verify_drafts", "verify_captured", "VerifyOutput", "Support", "support_of",
            "MAX_DRAFTS"]
@@ -32,6 +32,9 @@ class Support(NamedTuple):
     logprobs: torch.Tensor                  # float32 [N, P, W]
     lengths: torch.Tensor                   # int32 [N, P]
     status: Optional[torch.Tensor] = None   # int8 [N, P]; None: every slot is complete
+
+
+_NO_SUPPORT = Support(None, None, None)
 
 
 def support_of(out: SampleOutput, N: int) -> Support:
@@ -57,7 +60,7 @@ def _outputs(N: int, K: int, dev) -> VerifyOutput:
 def _check_requests(N, K, dev, draft_tokens, uniforms, seeds, positions, draft_counts) -> None:
     for t, name, dt in ((draft_tokens, "draft_tokens", torch.int32),
                         (uniforms, "uniforms", torch.float32)):
-        if t.device != dev or t.dtype != dt or tuple(t.shape) != (N, K) or not t.is_contiguous():
+        if t.shape != (N, K) or t.dtype != dt or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dt} tensor of shape [{N}, {K}] on {dev}")
     _check(seeds, "seeds", torch.int64, N, dev)
     _check(positions, "positions", torch.int64, N, dev)
@@ -66,7 +69,7 @@ def _check_requests(N, K, dev, draft_tokens, uniforms, seeds, positions, draft_c
 
 
 def _logits_3d(t: torch.Tensor, name: str, shape, dev) -> Tuple[int, int, int]:
-    if t.dim() != 3 or t.device != dev or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 3 or t.device != dev or (shape is not None and t.shape != shape):
         want = "[N, K + 1, V]" if shape is None else str(list(shape))
         raise ValueError(f"{name} must be {want} on {dev}")
     if t.shape[2] > 1 and t.stride(2) != 1:
@@ -102,16 +105,19 @@ def verify_drafts(target_logits: torch.Tensor, draft_tokens: torch.Tensor,
     d_dt = d_sn = d_sk = 0
     if draft_logits is not None:
         d_dt, d_sn, d_sk = _logits_3d(draft_logits, "draft_logits", (N, K, V), dev)
-    with _on_device(dev, stream) as s:
+    nbytes = lib.tsc_verify_drafts_workspace(N, K, V, draft_logits is not None)
+
+    def go(s):
         out = _outputs(N, K, dev)
-        nbytes = lib.tsc_verify_drafts_workspace(N, K, V, draft_logits is not None)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        code = lib.tsc_verify_drafts(
+        return out, lib.tsc_verify_drafts(
             target_logits.data_ptr(), t_dt, t_sn, t_sk, _ptr(draft_logits), d_dt, d_sn, d_sk, N, K,
             V, temperature.data_ptr(), _ptr(draft_temperature), draft_tokens.data_ptr(),
             _ptr(draft_counts), uniforms.data_ptr(), seeds.data_ptr(), positions.data_ptr(),
             out.tokens.data_ptr(), out.accepted.data_ptr(), out.logprobs.data_ptr(),
             out.row_status.data_ptr(), ws.data_ptr(), nbytes, s)
+
+    out, code = _launch(dev, stream, go)
     if code != 0:
         raise TscError(code, lib.tsc_status_string(code).decode(), "tsc_verify_drafts")
     return out
@@ -120,26 +126,28 @@ def verify_drafts(target_logits: torch.Tensor, draft_tokens: torch.Tensor,
 def _slots(sup: Support, name: str, N: int, P: int, dev) -> Tuple[int, int, int]:
     """(slot stride of requests, of positions, W) of a capture, after checking that its tensors
     share them."""
-    ids = sup.ids
-    if ids.dim() != 3 or tuple(ids.shape[:2]) != (N, P) or ids.shape[2] < 1:
+    ids, lps, lengths, status = sup
+    if ids.dim() != 3 or ids.shape[:2] != (N, P) or ids.shape[2] < 1:
         raise ValueError(f"{name}.ids must be [{N}, {P}, W]")
     W = ids.shape[2]
+    stride = lengths.stride()
     # The stride of an axis of one entry (or none) is never used.
-    sn = sup.lengths.stride(0) if N > 1 and sup.lengths.dim() == 2 else 0
-    sk = sup.lengths.stride(1) if P > 1 and sup.lengths.dim() == 2 else 0
-    for t, part, dt, inner in ((ids, "ids", torch.int32, W),
-                               (sup.logprobs, "logprobs", torch.float32, W),
-                               (sup.lengths, "lengths", torch.int32, 0),
-                               (sup.status, "status", torch.int8, 0)):
-        if t is None and part == "status":
-            continue
-        shape = (N, P, W) if inner else (N, P)
-        unit = inner if inner else 1
-        if (t.device != dev or t.dtype != dt or tuple(t.shape) != shape
-                or (inner > 1 and t.stride(2) != 1)
-                or (N > 1 and t.stride(0) != sn * unit) or (P > 1 and t.stride(1) != sk * unit)):
-            raise ValueError(f"{name}.{part} must be a {dt} tensor of shape {list(shape)} on {dev}, "
-                             "its slots laid out as those of lengths, its packed axis whole")
+    sn = stride[0] if N > 1 and len(stride) == 2 else 0
+    sk = stride[1] if P > 1 and len(stride) == 2 else 0
+
+    def laid(t, dt, shape, unit):
+        st = t.stride()
+        return (t.dtype == dt and t.shape == shape and t.device == dev
+                and (st == (sn * unit, sk * unit, 1)  # the usual case
+                     or ((N <= 1 or st[0] == sn * unit) and (P <= 1 or st[1] == sk * unit)
+                         and (W == 1 or len(st) == 2 or st[2] == 1))))
+
+    if not (laid(ids, torch.int32, (N, P, W), W) and laid(lps, torch.float32, (N, P, W), W)
+            and laid(lengths, torch.int32, (N, P), 1)
+            and (status is None or laid(status, torch.int8, (N, P), 1))):
+        raise ValueError(f"{name} must hold ids (int32) and logprobs (float32) of shape [{N}, {P}, W], "
+                         f"lengths (int32) and status (int8 or None) of shape [{N}, {P}], on {dev}, "
+                         "their slots laid out alike and the packed axis whole")
     return sn, sk, W
 
 
@@ -159,15 +167,18 @@ def verify_captured(target: Support, draft_tokens: torch.Tensor, uniforms: torch
     t_sn, t_sk, W = _slots(target, "target", N, K + 1, dev)
     d_sn, d_sk, Wd = (0, 0, 0) if draft is None else _slots(draft, "draft", N, K, dev)
     _check_requests(N, K, dev, draft_tokens, uniforms, seeds, positions, draft_counts)
-    d = draft if draft is not None else Support(None, None, None)
-    with _on_device(dev, stream) as s:
+    d = draft if draft is not None else _NO_SUPPORT
+
+    def go(s):
         out = _outputs(N, K, dev)
-        code = lib.tsc_verify_captured(
+        return out, lib.tsc_verify_captured(
             target.ids.data_ptr(), target.logprobs.data_ptr(), target.lengths.data_ptr(),
             _ptr(target.status), t_sn, t_sk, W, _ptr(d.ids), _ptr(d.logprobs), _ptr(d.lengths),
             _ptr(d.status), d_sn, d_sk, Wd, N, K, draft_tokens.data_ptr(), _ptr(draft_counts),
             uniforms.data_ptr(), seeds.data_ptr(), positions.data_ptr(), out.tokens.data_ptr(),
             out.accepted.data_ptr(), out.logprobs.data_ptr(), out.row_status.data_ptr(), s)
+
+    out, code = _launch(dev, stream, go)
     if code != 0:
         raise TscError(code, lib.tsc_status_string(code).decode(), "tsc_verify_captured")
     return out
