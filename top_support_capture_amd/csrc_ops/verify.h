@@ -101,16 +101,13 @@ __device__ inline uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
   return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
 }
 
-// Words of the groups of four ids from `group` on, under counter word 1 = `stream`.
+// Words of N groups of four ids (id / 4, in out[i][0] at first), under counter word 1 = `stream`.
 template <int N>
-__device__ inline void race_words(uint32_t group, uint32_t stream, uint64_t seed, uint64_t position,
-                                  uint32_t (&out)[N][4]) {
+__device__ inline void race_words(uint32_t stream, uint64_t seed, uint64_t position, uint32_t (&out)[N][4]) {
   uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    out[i][0] = group + (uint32_t)i, out[i][1] = stream;
-    out[i][2] = (uint32_t)position, out[i][3] = (uint32_t)(position >> 32);
-  }
+  for (int i = 0; i < N; ++i)
+    out[i][1] = stream, out[i][2] = (uint32_t)position, out[i][3] = (uint32_t)(position >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
 #pragma unroll
@@ -123,11 +120,15 @@ __device__ inline void race_words(uint32_t group, uint32_t stream, uint64_t seed
   }
 }
 
-__device__ inline uint32_t race_word(uint32_t id, uint32_t stream, uint64_t seed, uint64_t position) {
-  uint32_t w[1][4];
-  race_words(id >> 2, stream, seed, position, w);
+__device__ inline uint32_t word_of(const uint32_t (&w)[4], uint32_t id) {
   const uint32_t j = id & 3u;
-  return j == 0 ? w[0][0] : j == 1 ? w[0][1] : j == 2 ? w[0][2] : w[0][3];
+  return j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3];
+}
+
+__device__ inline uint32_t race_word(uint32_t id, uint32_t stream, uint64_t seed, uint64_t position) {
+  uint32_t w[1][4] = {{id >> 2}};
+  race_words(stream, seed, position, w);
+  return word_of(w[0], id);
 }
 
 // t = 1 - u of a Philox word: u = (2 (word >> 9) + 1) / 2^24, all exact in float32.
@@ -366,8 +367,8 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
     }
     // t is at least 2^-24: below that share of the bound no word wins, and none is drawn.
     if (__ballot(most > bound * 0x1p-24f) == 0) return;
-    uint32_t word[2][4];
-    race_words(((uint32_t)at) >> 2, stream, seed, position, word);
+    uint32_t word[2][4] = {{(uint32_t)at >> 2}, {((uint32_t)at >> 2) + 1u}};
+    race_words(stream, seed, position, word);
     float tt[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) tt[e] = race_t(word[e >> 2][e & 3]);
@@ -477,7 +478,7 @@ struct CapturedArgs {
   int8_t* row_status;  // [N]
 };
 
-constexpr int kCapThreads = 512;
+constexpr int kCapThreads = 1024;
 constexpr int kCapWaves = kCapThreads / kWaveSize;
 
 // The slot's status: a capture that is not whole cannot be verified against.
@@ -523,23 +524,31 @@ __global__ void __launch_bounds__(kCapThreads) verify_captured_kernel(CapturedAr
   for (int32_t i = (int32_t)tid; i < count; i += kCapThreads)
     lp_t[i] = -__builtin_inff(), lp_d[i] = has_draft ? -__builtin_inff() : 0.0f;
   lds_barrier();
-  // The drafts' logprobs in both lists (-inf where they are not in them).
-  for (int32_t j = w; j < (has_draft ? 2 : 1) * count; j += kCapWaves) {
+  // The drafts' logprobs in both lists (-inf where they are not in them): a list to a wave, or to
+  // several where there are more waves than lists.
+  const int32_t lists = (has_draft ? 2 : 1) * count;
+  const int32_t parts = lists > 0 && lists < kCapWaves ? kCapWaves / lists : 1;
+  for (int32_t k = w; k < lists * parts; k += kCapWaves) {
+    const int32_t j = k % lists, part = k / lists;
     const bool is_draft = j >= count;
     const int32_t i = is_draft ? j - count : j;
     const SupportArgs& s = is_draft ? a.draft : a.target;
     const int64_t slot = n * s.sn + i * s.sk;
+    const int32_t want = a.draft_tokens[n * K + i];
     if (slot_status(s, slot) != TSC_ROW_OK) continue;
-    const int32_t len = s.lengths[slot], want = a.draft_tokens[n * K + i];
+    const int32_t len = s.lengths[slot];
     const int32_t* ids = s.ids + slot * s.W;
     constexpr int kU = 8;
-    for (int32_t e0 = (int32_t)lane; e0 < len; e0 += kWaveSize * kU) {
+    for (int32_t e0 = part * kWaveSize + (int32_t)lane; e0 - (int32_t)lane < len; e0 += parts * kWaveSize * kU) {
       int32_t id[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) id[u] = e0 + u * kWaveSize < len ? ids[e0 + u * kWaveSize] : ~want;
+      for (int u = 0; u < kU; ++u) {
+        const int32_t e = e0 + u * parts * kWaveSize;
+        id[u] = e < len ? ids[e] : ~want;
+      }
 #pragma unroll
       for (int u = 0; u < kU; ++u)
-        if (id[u] == want) (is_draft ? lp_d : lp_t)[i] = s.logprobs[slot * s.W + e0 + u * kWaveSize];
+        if (id[u] == want) (is_draft ? lp_d : lp_t)[i] = s.logprobs[slot * s.W + e0 + u * parts * kWaveSize];
     }
   }
   lds_barrier();
@@ -566,6 +575,20 @@ __global__ void __launch_bounds__(kCapThreads) verify_captured_kernel(CapturedAr
   const int32_t t_len = a.target.lengths[t_slot];
   const int32_t* t_ids = a.target.ids + t_slot * a.target.W;
   const float* t_lps = a.target.logprobs + t_slot * a.target.W;
+  const uint64_t seed = a.seeds[n], position = a.positions[n] + (uint64_t)stop;
+  // kU entries of a thread at a time: what their lists hold is asked for together.
+  constexpr int kU = 4;
+  int32_t id[kU];
+  float lp[kU];
+  auto load_entries = [&](int32_t e0) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int32_t e = e0 + u * kCapThreads;
+      id[u] = e < t_len ? t_ids[e] : -1;
+      lp[u] = e < t_len ? t_lps[e] : -__builtin_inff();
+    }
+  };
+  load_entries((int32_t)tid);
   const int32_t* d_ids = nullptr;
   const float* d_lps = nullptr;
   uint32_t mask = 0;
@@ -577,44 +600,78 @@ __global__ void __launch_bounds__(kCapThreads) verify_captured_kernel(CapturedAr
     uint32_t slots = 64;  // a power of two, at least twice the entries: every probe ends
     while (slots < 2u * (uint32_t)d_len) slots <<= 1;
     mask = slots - 1u;
+    int32_t mine[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      mine[u] = (int32_t)tid + u * kCapThreads < d_len ? d_ids[tid + u * kCapThreads] : -1;
     for (uint32_t i = tid; i < slots; i += kCapThreads) table[i] = 0u;
     lds_barrier();
     // A slot holds the entry's index + 1 (at most 16384) and 17 bits of the id's hash beside it, so
     // that an entry of another id rarely costs a read of its id.
-    for (int32_t e = (int32_t)tid; e < d_len; e += kCapThreads) {
-      const uint32_t h = id_hash(d_ids[e]);
+    auto insert = [&](int32_t e, int32_t of) {
+      const uint32_t h = id_hash(of);
       const uint32_t v = (h << 15) | (uint32_t)(e + 1);
       uint32_t at = (h >> 17) & mask;
       while (atomicCAS(&table[at], 0u, v) != 0u) at = (at + 1u) & mask;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if ((int32_t)tid + u * kCapThreads < d_len) insert((int32_t)tid + u * kCapThreads, mine[u]);
+    for (int32_t e = (int32_t)tid + kU * kCapThreads; e < d_len; e += kCapThreads) insert(e, d_ids[e]);
     lds_barrier();
   }
-  const uint64_t seed = a.seeds[n], position = a.positions[n] + (uint64_t)stop;
-  auto exact = [](float lp, float lq) -> double { return exp((double)lp) - exp((double)lq); };
+  auto exact = [](float x, float y) -> double { return exp((double)x) - exp((double)y); };
   RaceEntry best;
-  for (int32_t e = (int32_t)tid; e < t_len; e += kCapThreads) {
-    const int32_t id = t_ids[e];
-    const float lp = t_lps[e];
-    float lq = -__builtin_inff();
-    if (subtract) {
-      const uint32_t h = id_hash(id);
-      for (uint32_t at = (h >> 17) & mask;; at = (at + 1u) & mask) {
-        const uint32_t v = table[at];
-        if (v == 0u) break;
-        if ((v >> 15) == (h & 0x1FFFFu) && d_ids[(v & 0x7FFFu) - 1u] == id) {
-          lq = d_lps[(v & 0x7FFFu) - 1u];
-          break;
+  for (int32_t e0 = (int32_t)tid;; e0 += kU * kCapThreads) {
+    float lq[kU];
+    uint32_t word[kU][4];
+    // The place an id's probe stops at: its entry, unless another id shares its 17 bits.
+    uint32_t at[kU], found[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      lq[u] = -__builtin_inff();
+      word[u][0] = (uint32_t)id[u] >> 2;
+      found[u] = 0u;
+      if (subtract && e0 + u * kCapThreads < t_len) {
+        const uint32_t h = id_hash(id[u]);
+        at[u] = (h >> 17) & mask;
+        for (uint32_t v; (v = table[at[u]]) != 0u; at[u] = (at[u] + 1u) & mask) {
+          if ((v >> 15) == (h & 0x1FFFFu)) {
+            found[u] = v & 0x7FFFu;
+            break;
+          }
         }
       }
-    } else if (id == drafted) {
-      continue;
     }
-    const float p = exp_fast(lp), q = exp_fast(lq), wt = p - q;
-    if (wt > 0.0f || RaceEntry::race_near(p, wt)) {
-      const float tt = race_t(race_word((uint32_t)id, rejected ? 1u : 0u, seed, position));
-      if (RaceEntry::can_win(p, wt, tt, best.score * (1.0f - kRaceClose)))
-        best.offer(p, q, id, tt, lp, lq, exact);
+    int32_t other[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      other[u] = found[u] != 0u ? d_ids[found[u] - 1u] : id[u];
+      if (found[u] != 0u) lq[u] = d_lps[found[u] - 1u];
     }
+    race_words(rejected ? 1u : 0u, seed, position, word);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (e0 + u * kCapThreads >= t_len) continue;
+      if (other[u] != id[u]) {  // another id of the same 17 bits: on with the probe
+        lq[u] = -__builtin_inff();
+        const uint32_t h = id_hash(id[u]);
+        for (uint32_t v; (v = table[at[u] = (at[u] + 1u) & mask]) != 0u;) {
+          const uint32_t f = v & 0x7FFFu;
+          if ((v >> 15) == (h & 0x1FFFFu) && d_ids[f - 1u] == id[u]) {
+            lq[u] = d_lps[f - 1u];
+            break;
+          }
+        }
+      }
+      if (!subtract && id[u] == drafted) continue;
+      const float p = exp_fast(lp[u]), q = exp_fast(lq[u]);
+      const float tt = race_t(word_of(word[u], (uint32_t)id[u]));
+      if (RaceEntry::can_win(p, p - q, tt, best.score * (1.0f - kRaceClose)))
+        best.offer(p, q, id[u], tt, lp[u], lq[u], exact);
+    }
+    if (e0 - (int32_t)tid + kU * kCapThreads >= t_len) break;
+    load_entries(e0 + kU * kCapThreads);
   }
   const RacePart won = race_winner<kCapWaves>(best, exact, sh_score, sh_best);
   // No token with p > q: the two distributions agree within rounding, and the draft is as good a
