@@ -46,9 +46,9 @@ Cut loss_cut(int64_t N, int64_t V) {
   return N >= 256 || V <= 65536 ? Cut{1, V} : stats_cut(N, V);
 }
 // Gradients: segments of rows, as long as their windows allow unless there are few rows.
-Cut grad_cut(int64_t N, int64_t V) {
+Cut grad_cut(int64_t N, int64_t V, int64_t target) {
   constexpr int64_t unit = tsc::Window<tsc::kGradThreads>::kSize;
-  int64_t len = ceil_div(ceil_div(V, ceil_div(512, N)), unit) * unit;
+  int64_t len = ceil_div(ceil_div(V, ceil_div(target, N)), unit) * unit;
   if (len > tsc::kMaxSegment) len = tsc::kMaxSegment;
   return {(int32_t)ceil_div(V, len), len};
 }
@@ -147,10 +147,8 @@ template <int kThr, class Args>
 hipError_t launch_grad(void (*kernel)(Args), const Args& a, int64_t groups, std::atomic<uint64_t>& allowed,
                        hipStream_t s) {
   using Ent = tsc::Entries<kThr>;
-  constexpr size_t most = Ent::bytes(TSC_MAX_PACKED_WIDTH) > Ent::bytes(Ent::kMostForTwo)
-                              ? Ent::bytes(TSC_MAX_PACKED_WIDTH) : Ent::bytes(Ent::kMostForTwo);
-  static_assert(most <= 156 * 1024, "beside the kernels' static LDS");
-  const hipError_t err = allow_lds(kernel, most, allowed);
+  static_assert(Ent::bytes(TSC_MAX_PACKED_WIDTH) <= (size_t)Ent::kAll, "the widest rows fit");
+  const hipError_t err = allow_lds(kernel, (size_t)Ent::kAll, allowed);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThr), Ent::bytes(a.W), s, a);
   return hipGetLastError();
@@ -303,7 +301,7 @@ int32_t tsc_distill_topk_backward(const void* logits, int32_t dtype, int64_t N, 
   if (!temperature || !teacher_ids || !teacher_values || !lengths || !stats || !grad_loss ||
       !grad_logits || !aligned(grad_logits, dtype))
     return TSC_ERR_INVALID_ARGUMENT;
-  const Cut cut = grad_cut(N, V);
+  const Cut cut = grad_cut(N, V, 512);
   const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
                            teacher_temperature, nullptr, nullptr, const_cast<float*>(stats), nullptr,
                            0, 0, grad_loss, grad_logits, cut.n, cut.len};
@@ -324,7 +322,7 @@ int32_t tsc_distill_topk_grad(const void* logits, int32_t dtype, int64_t N, int6
     return TSC_ERR_INVALID_ARGUMENT;
   if (const int32_t e = check_workspace(workspace, workspace_bytes, distill_grad_bytes(N, V))) return e;
   const bool one = fused(N, V);
-  const Cut cut = one ? Cut{1, V} : loss_cut(N, V), seg = grad_cut(N, V);
+  const Cut cut = one ? Cut{1, V} : loss_cut(N, V), seg = grad_cut(N, V, 512);
   char* stats = static_cast<char*>(workspace) + distill_bytes(N, V);
   const tsc::DistillArgs a{logits, N, V, ld, temperature, teacher_ids, teacher_values, lengths, W,
                            teacher_temperature, loss, row_status, reinterpret_cast<float*>(stats),
@@ -354,7 +352,7 @@ int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N
   if (!temperature || !packed_ids || !lengths || !tokens || !grad_logits ||
       !aligned(grad_logits, dtype) || (support_bits && bits_ld < (V + 7) / 8))
     return TSC_ERR_INVALID_ARGUMENT;
-  const Cut cut = grad_cut(N, V);
+  const Cut cut = grad_cut(N, V, 256);
   const tsc::ReplayGradArgs a{logits, N, V, ld, temperature, packed_ids, lengths, W, capture_status,
                               support_bits, bits_ld, tokens, grad_selected, grad_logprobs,
                               grad_logits, cut.n, cut.len};

@@ -41,18 +41,89 @@ __device__ inline void fill_zero(typename Row<DT>::Bits* out, int64_t lo, int64_
     store8<DT>(out, at, hi, zero);
 }
 
+struct ReplayShared {
+  float m[kGradWaves];
+  uint32_t f[kGradWaves];
+  double s[kGradWaves], g[kGradWaves];
+};
+
+// Entries i0, i0 + kGradThreads, ... of a packed row: ids, upstream gradients and logits (id -1 past
+// the length).
+template <int DT, int N>
+struct PackedEntries {
+  static constexpr int kE = N;
+  int32_t id[N];
+  float up[N], x[N];
+  __device__ inline void load(const int32_t* ids, const float* gl, const typename Row<DT>::Bits* row, int64_t V,
+                              int32_t len, int32_t i0) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      id[u] = i0 + u * kGradThreads < len ? ids[i0 + u * kGradThreads] : -1;
+      up[u] = gl && i0 + u * kGradThreads < len ? gl[i0 + u * kGradThreads] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) x[u] = id[u] >= 0 && id[u] < V ? Row<DT>::get(row + id[u]) : -__builtin_inff();
+  }
+};
+
+// Mask bytes and logits of a bitmask row, kAhead windows before their turn. Lanes past the last
+// whole chunk of [lo, hi) ask for the first one, and use nothing of it.
 template <int DT>
-__global__ void __launch_bounds__(kGradThreads, 8) replay_grad_kernel(ReplayGradArgs a) {
+struct MaskedStream {
+  static constexpr int kSize = Window<kGradThreads>::kSize;
+  static constexpr int kAhead = DT == TSC_DTYPE_BF16 ? 4 : 2;
+  const typename Row<DT>::Bits* row;
+  const uint8_t* bits;
+  int64_t lo, hi;
+  typename Row<DT>::Chunk v[kAhead];
+  uint32_t b[kAhead];
+  __device__ inline int64_t place(int k) const { return lo + (int64_t)k * kSize + (int64_t)threadIdx.x * 8; }
+  __device__ inline void ask(int j, int k) {
+    if (lo + 8 > hi) return;
+    const int64_t at = place(k) + 8 <= hi ? place(k) : lo;
+    b[j] = bits[at >> 3];
+    v[j] = Row<DT>::load(row + at);
+  }
+  // use(k, at, x, mask) for every window k of the segment, the logits of non-members as they are.
+  template <class Use>
+  __device__ inline void run(Use use) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) ask(j, j);
+    for (int k0 = 0; lo + (int64_t)k0 * kSize < hi; k0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = k0 + j;
+        if (lo + (int64_t)k * kSize < hi) {  // uniform
+          const int64_t at = place(k);
+          float x[8];
+          uint32_t mask = b[j];
+          if (at + 8 <= hi) {
+            Row<DT>::unpack(v[j], x);
+          } else {
+            load8<DT>(row, at, hi, x);
+            mask = at < hi ? bits[at >> 3] & ((1u << (hi - at)) - 1u) : 0u;
+          }
+          ask(j, k + kAhead);
+          use(k, at, x, mask);
+        }
+      }
+    }
+  }
+};
+
+// All ones where bit e of b is set: members are kept by masks, not by branches.
+__device__ inline uint32_t member_mask(uint32_t b, int e) { return (uint32_t)((int32_t)(b << (31 - e)) >> 31); }
+
+template <int DT>
+__global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGradArgs a) {
   using B = typename Row<DT>::Bits;
   extern __shared__ __attribute__((aligned(16))) float dyn_lds[];
-  __shared__ float sh_m[kGradWaves];
-  __shared__ double sh_s[kGradWaves], sh_g[kGradWaves];
-  __shared__ uint32_t sh_f[kGradWaves];
+  __shared__ ReplayShared sh;
   const Entries<kGradThreads> ent(dyn_lds, a.W);
   const int64_t n = blockIdx.x / a.segments;
   const int64_t lo = (blockIdx.x - n * a.segments) * a.seg_len;
   const int64_t hi = lo + a.seg_len < a.V ? lo + a.seg_len : a.V;
-  const int32_t tid = (int32_t)threadIdx.x;
+  const int32_t tid = (int32_t)threadIdx.x, lane = tid & (kWaveSize - 1), w = tid / kWaveSize;
   const float T = a.temperature[n];
   const int32_t len = a.lengths[n], tok = a.tokens[n];
   const int32_t cs = a.capture_status ? (int32_t)a.capture_status[n] : TSC_ROW_OK;
@@ -71,98 +142,126 @@ __global__ void __launch_bounds__(kGradThreads, 8) replay_grad_kernel(ReplayGrad
   const float* gl = a.grad_logprobs ? a.grad_logprobs + n * a.W : nullptr;
   const bool entries = !from_bits || (gl != nullptr && len_ok);  // the packed ids take part
 
-  // Entries of the packed row, kE per thread at a time: the first batch stays in registers.
-  constexpr int kE = 4;
-  constexpr int kBatch = kGradThreads * kE;
-  int32_t id[kE];
-  float x[kE], up[kE];
-  auto load_entries = [&](int32_t i0) {
-#pragma unroll
-    for (int u = 0; u < kE; ++u) id[u] = i0 + u * kGradThreads < len ? ids[i0 + u * kGradThreads] : -1;
-#pragma unroll
-    for (int u = 0; u < kE; ++u) {
-      up[u] = gl && i0 + u * kGradThreads < len ? gl[i0 + u * kGradThreads] : 0.0f;
-      x[u] = id[u] >= 0 && id[u] < a.V ? Row<DT>::get(row + id[u]) : -__builtin_inff();
-    }
+  // Entries of the packed row: a thread's first kFirst stay in registers, the rest come kMore at a
+  // time, all of their loads together, and are read again when they are placed.
+  constexpr int kFirst = 2, kMore = 6;
+  PackedEntries<DT, kFirst> first;
+  // Whether entry u is of the support and, if so, of this segment.
+  auto of_support = [&](int32_t id) {
+    return id >= 0 && id < a.V && (!from_bits || ((bits[id >> 3] >> (id & 7)) & 1u));
   };
+  auto here = [&](int32_t id) { return id >= lo && id < hi && of_support(id); };
   LseState st;
   double G = 0.0;
   uint32_t flags = 0;  // 1: an id out of range, 2: an element of the support, 4: the token is one
-  if (entries) load_entries(tid);
+  if (entries) first.load(ids, gl, row, a.V, len, tid);
   ent.begin();
   lds_barrier();
-  if (entries) {
-    for (int32_t i0 = tid;; i0 += kBatch) {
-      if (!from_bits) st.add(x, c);
+  auto look = [&](auto& t, int32_t i0) {
+    if (!from_bits) st.add(t.x, c);
 #pragma unroll
-      for (int u = 0; u < kE; ++u) {
-        const bool in = id[u] >= 0 && id[u] < a.V;
-        if (!from_bits && i0 + u * kGradThreads < len) flags |= !in ? 1u : id[u] == tok ? 6u : 2u;
-        if (!in || (from_bits && !((bits[id[u] >> 3] >> (id[u] & 7)) & 1u))) continue;
-        G += (double)up[u];
-        if (id[u] >= lo && id[u] < hi) ent.count((uint32_t)(id[u] - lo));
-      }
-      if (i0 - tid + kBatch >= len) break;
-      load_entries(i0 + kBatch);
+    for (int u = 0; u < t.kE; ++u) {
+      const int32_t id = t.id[u];
+      if (!from_bits && i0 + u * kGradThreads < len) flags |= id < 0 || id >= a.V ? 1u : id == tok ? 6u : 2u;
+      if (of_support(id)) G += (double)t.up[u];
+      if (here(id)) ent.count((uint32_t)(id - lo));
+    }
+  };
+  if (entries) {
+    look(first, tid);
+    for (int32_t i0 = tid + kFirst * kGradThreads; i0 - tid < len; i0 += kMore * kGradThreads) {
+      PackedEntries<DT, kMore> t;
+      t.load(ids, gl, row, a.V, len, i0);
+      look(t, i0);
     }
   }
   if (from_bits) {
     // The whole row and its mask are streamed: where members are so many that they did not fit
     // the packed width, hardly a line of the row is without one.
-    constexpr int kU = 4;
-    const int64_t full = a.V / 8;
-    auto add_chunk = [&](uint32_t b, float (&v)[8], int64_t ch) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!((b >> e) & 1u)) v[e] = -__builtin_inff();
-      st.add(v, c);
-      flags |= (b != 0u ? 2u : 0u) | (ch == tok >> 3 && ((b >> (tok & 7)) & 1u) ? 4u : 0u);
+    constexpr int kU = DT == TSC_DTYPE_BF16 ? 4 : 2;  // chunks of a thread at a time, and as many ahead
+    constexpr int64_t kStep = kGradThreads * 8;
+    const int64_t whole = a.V & ~int64_t{7}, start = (int64_t)tid * 8;
+    typename Row<DT>::Chunk v[kU];
+    uint32_t b[kU], any = 0;
+    auto ask = [&](int u, int64_t at) {  // past the last whole chunk: the first one, without members
+      const bool in = at < whole;
+      b[u] = bits[in ? at >> 3 : 0];
+      v[u] = Row<DT>::load(row + (in ? at : 0));
+      if (!in) b[u] = 0u;
     };
-    int64_t ch0 = 0;
-    for (; ch0 + kU * kGradThreads <= full; ch0 += kU * kGradThreads) {
-      uint32_t b[kU];
-      typename Row<DT>::Chunk v[kU];
+    if (whole > 0) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) b[u] = bits[ch0 + u * kGradThreads + tid];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] = Row<DT>::load(row + (ch0 + u * kGradThreads) * 8 + tid * 8);
+      for (int u = 0; u < kU; ++u) ask(u, start + u * kStep);
+    }
+    for (int64_t base = 0; base < whole; base += kU * kStep) {
+      float f[kU * 8];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        float f[8];
-        Row<DT>::unpack(v[u], f);
-        add_chunk(b[u], f, ch0 + u * kGradThreads + tid);
+        Row<DT>::unpack(v[u], reinterpret_cast<float(&)[8]>(f[u * 8]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t keep = member_mask(b[u], e);
+          f[u * 8 + e] = __uint_as_float((__float_as_uint(f[u * 8 + e]) & keep) | (0xFF800000u & ~keep));
+        }
+        any |= b[u];
+        ask(u, base + start + (kU + u) * kStep);
       }
+      st.add(f, c);
     }
-    for (int64_t ch = ch0 + tid; ch * 8 < a.V; ch += kGradThreads) {
+    if (whole < a.V && tid == 0) {  // the ragged last chunk
+      const uint32_t last = bits[whole >> 3] & ((1u << (a.V & 7)) - 1u);
       float f[8];
-      load8<DT>(row, ch * 8, a.V, f);
-      add_chunk(ch < full ? bits[ch] : bits[ch] & ((1u << (a.V & 7)) - 1u), f, ch);
+      load8<DT>(row, whole, a.V, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!((last >> e) & 1u)) f[e] = -__builtin_inff();
+      st.add(f, c);
+      any |= last;
     }
+    flags |= (any != 0u ? 2u : 0u) | ((bits[tok >> 3] >> (tok & 7)) & 1u ? 4u : 0u);
   }
-  block_lse<kGradWaves>(st.m, st.s, c, sh_m, sh_s);
-  G = block_all<kGradWaves>(G, SumOp(), sh_g);
-  flags = block_all<kGradWaves>(flags, [](uint32_t p, uint32_t q) { return p | q; }, sh_f);
-  if (!((flags & 3u) == 2u && st.s < __builtin_inf() && __builtin_fabsf(st.m) < __builtin_inff())) {
+  // The workgroup's maximum and flags, then its sums; between the two barriers the first wave
+  // also turns the windows' counts into offsets.
+  const float wm = wave_max(st.m);
+  flags = wave_reduce(flags, [](uint32_t p, uint32_t q) { return p | q; });
+  if (lane == 0) sh.m[w] = wm, sh.f[w] = flags;
+  lds_barrier();
+  float m = sh.m[0];
+  flags = sh.f[0];
+#pragma unroll
+  for (int i = 1; i < kGradWaves; ++i) m = __builtin_fmaxf(m, sh.m[i]), flags |= sh.f[i];
+  const double ws = wave_reduce(rescaled(st.s, st.m, m, c), SumOp());
+  G = wave_reduce(G, SumOp());
+  if (lane == 0) sh.s[w] = ws, sh.g[w] = G;
+  ent.offsets();
+  lds_barrier();
+  double S = sh.s[0];
+  G = sh.g[0];
+#pragma unroll
+  for (int i = 1; i < kGradWaves; ++i) S += sh.s[i], G += sh.g[i];
+  if (!((flags & 3u) == 2u && S < __builtin_inf() && __builtin_fabsf(m) < __builtin_inff())) {
     fill_zero<DT, kGradThreads>(out, lo, hi);
     return;
   }
   const float gs = a.grad_selected && (flags & 4u) ? a.grad_selected[n] : 0.0f;
   G += (double)gs;
-  const float inv_T = 1.0f / T, m = st.m;
-  const float share = (float)(G / ((double)T * st.s));  // sum of G over T s
+  const float inv_T = 1.0f / T;
+  const float share = (float)(G / ((double)T * S));  // sum of G over T s
   // What a packed id adds: all of a packed row's gradient, the upstream gradient alone of a
   // bitmask row's, whose other term comes with the stream.
-  ent.offsets();
-  lds_barrier();
-  if (entries) {
-    for (int32_t i0 = tid; i0 - tid < len; i0 += kBatch) {
-      if (len > kBatch) load_entries(i0);
+  auto place = [&](const auto& t) {
 #pragma unroll
-      for (int u = 0; u < kE; ++u) {
-        if (id[u] < lo || id[u] >= hi || (from_bits && !((bits[id[u] >> 3] >> (id[u] & 7)) & 1u))) continue;
-        const float own = from_bits ? 0.0f : exp2_scaled(x[u] - m, c) * share;
-        ent.place((uint32_t)(id[u] - lo), up[u] * inv_T - own);
-      }
+    for (int u = 0; u < t.kE; ++u)
+      if (here(t.id[u]))
+        ent.place((uint32_t)(t.id[u] - lo),
+                  t.up[u] * inv_T - (from_bits ? 0.0f : exp2_scaled(t.x[u] - m, c) * share));
+  };
+  if (entries) {
+    place(first);
+    for (int32_t i0 = tid + kFirst * kGradThreads; i0 - tid < len; i0 += kMore * kGradThreads) {
+      PackedEntries<DT, kMore> t;
+      t.load(ids, gl, row, a.V, len, i0);
+      place(t);
     }
   }
   lds_barrier();
@@ -172,25 +271,49 @@ __global__ void __launch_bounds__(kGradThreads, 8) replay_grad_kernel(ReplayGrad
     if (tid == 0 && tok >= lo && tok < hi && (tok - lo) / kSize == k)
       ent.at_window(k).add((uint32_t)((tok - lo) % kSize), gs * inv_T);
   };
-  add(0);
-  lds_barrier();
-  for (int k = 0; lo + (int64_t)k * kSize < hi; ++k) {
-    const int64_t at = lo + (int64_t)k * kSize + tid * 8;
-    uint32_t b = 0u;
-    float v[8];
-    if (from_bits && at < hi) {
-      b = bits[at >> 3];
-      load8<DT>(row, at, hi, v);
+  if (entries) {
+    add(0);
+    lds_barrier();
+  }
+  if (!from_bits) {
+    for (int k = 0; lo + (int64_t)k * kSize < hi; ++k) {
+      ent.turn(k, add, [&] {
+        const int64_t at = lo + (int64_t)k * kSize + tid * 8;
+        if (at >= hi) return;
+        float r[8];
+        ent.at_window(k).take(tid, r);
+        store8<DT>(out, at, hi, r);
+      });
     }
-    ent.turn(k, add, [&] {
-      if (at >= hi) return;
-      float r[8];
-      ent.at_window(k).take(tid, r);
-      if (from_bits) {
+    return;
+  }
+  // Of a member the stream gives -pi sum of G / T; `r` holds what the entries add to it.
+  auto write = [&](int64_t at, const float (&v)[8], uint32_t b, float (&r)[8]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = (b >> e) & 1u ? r[e] - exp2_scaled(v[e] - m, c) * share : 0.0f;
+    for (int e = 0; e < 8; ++e)
+      r[e] = __uint_as_float(__float_as_uint(__builtin_fmaf(exp2_scaled(v[e] - m, c), -share, r[e])) &
+                             member_mask(b, e));
+    store8<DT>(out, at, hi, r);
+  };
+  MaskedStream<DT> stream{row, bits, lo, hi};
+  if (entries) {
+    stream.run([&](int k, int64_t at, float (&v)[8], uint32_t b) {
+      ent.turn(k, add, [&] {
+        if (at >= hi) return;
+        float r[8];
+        ent.at_window(k).take(tid, r);
+        write(at, v, b, r);
+      });
+    });
+  } else {  // the token alone has an upstream gradient: no windows, no barriers
+    stream.run([&](int, int64_t at, float (&v)[8], uint32_t b) {
+      if (at >= hi) return;
+      float r[8] = {};
+      if (at >> 3 == tok >> 3) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = e == (tok & 7) ? gs * inv_T : 0.0f;
       }
-      store8<DT>(out, at, hi, r);
+      write(at, v, b, r);
     });
   }
 }

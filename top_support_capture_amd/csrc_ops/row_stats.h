@@ -269,48 +269,61 @@ struct Window {
   }
 };
 
-// LDS of a workgroup that writes such rows: two windows, which take turns so that one barrier
-// separates a window's entries from its chunks, and the entries; one window alone where with two
-// the space for the entries would keep a second workgroup off the CU.
+// LDS of a workgroup that writes such rows: the entries, and two windows, which take turns so that
+// one barrier separates a window's entries from its chunks; or one window, where that lets a second
+// workgroup on the CU, or where two do not fit.
 template <int kThr>
 struct Entries {
   static constexpr int kSize = Window<kThr>::kSize;
-  static constexpr int64_t kFixed = (2 * kMaxWindows + 4) * 4;
-  static constexpr int64_t kMostForTwo = (78 * 1024 - kFixed - 2 * kSize * 4) / 6;  // entries
+  // Counters of a window: lanes that count into the same window at the same time mostly meet
+  // different ones.
+  static constexpr int kCopies = 4;
+  static constexpr int64_t kFixed = (kMaxWindows + 4 + kMaxWindows * kCopies) * 4;
+  static constexpr int64_t kHalf = 78 * 1024, kAll = 156 * 1024;  // of a CU's LDS, beside static LDS
   bool two;
   float* window;     // [1 or 2][kSize]
-  float* val;        // [W]
   uint32_t* start;   // [kMaxWindows + 1]
-  uint32_t* cursor;  // [kMaxWindows]
+  uint32_t* cursor;  // [kMaxWindows][kCopies]
+  float* val;        // [W]
   uint16_t* rel;     // [W]
-  __host__ __device__ static constexpr size_t bytes(int64_t W) {
-    return (W <= kMostForTwo ? 2 : 1) * kSize * 4 + W * 4 + kFixed + (W + 1) / 2 * 4;
+  __host__ __device__ static constexpr int64_t with(int windows, int64_t W) {
+    return windows * kSize * 4 + W * 4 + kFixed + (W + 1) / 2 * 4;
   }
+  __host__ __device__ static constexpr bool takes_two(int64_t W) {
+    return with(2, W) <= (with(1, W) <= kHalf ? kHalf : kAll);
+  }
+  __host__ __device__ static constexpr size_t bytes(int64_t W) { return (size_t)with(takes_two(W) ? 2 : 1, W); }
   __device__ inline explicit Entries(void* lds, int32_t W) {
-    two = W <= kMostForTwo;
+    two = takes_two(W);
     window = reinterpret_cast<float*>(lds);
-    val = window + (two ? 2 : 1) * kSize;
-    start = reinterpret_cast<uint32_t*>(val + W);
-    cursor = start + kMaxWindows + 4;
-    rel = reinterpret_cast<uint16_t*>(cursor + kMaxWindows);
+    start = reinterpret_cast<uint32_t*>(window + (two ? 2 : 1) * kSize);
+    cursor = start + kMaxWindows + 4;  // 16-byte aligned, as `lds` and the window's size are
+    val = reinterpret_cast<float*>(cursor + kMaxWindows * kCopies);
+    rel = reinterpret_cast<uint16_t*>(val + W);
   }
   // In this order, with a barrier between any two: begin, count of every entry, offsets, place of
   // every entry. `at` counts from the segment's first element and is below kMaxWindows * kSize.
   __device__ inline void begin() const {
     Window<kThr>{window}.clear();
     if (two) Window<kThr>{window + kSize}.clear();
-    if (threadIdx.x < kMaxWindows) cursor[threadIdx.x] = 0u;
+    if (threadIdx.x < kMaxWindows * kCopies) cursor[threadIdx.x] = 0u;
   }
-  __device__ inline void count(uint32_t at) const { atomicAdd(&cursor[at / kSize], 1u); }
+  __device__ inline uint32_t* counter(uint32_t at) const {
+    return &cursor[at / kSize * kCopies + (threadIdx.x & (kCopies - 1))];
+  }
+  __device__ inline void count(uint32_t at) const { atomicAdd(counter(at), 1u); }
   __device__ inline void offsets() const {
-    if (threadIdx.x < kMaxWindows) {  // the first wave
-      const uint32_t n = cursor[threadIdx.x], incl = wave_incl_scan(n, SumOp(), 0u);
-      start[threadIdx.x] = cursor[threadIdx.x] = incl - n;
+    if (threadIdx.x < kMaxWindows) {  // the first wave, a window per lane
+      uint4 n = *reinterpret_cast<uint4*>(cursor + threadIdx.x * kCopies);
+      const uint32_t sum = n.x + n.y + n.z + n.w, incl = wave_incl_scan(sum, SumOp(), 0u), at = incl - sum;
+      start[threadIdx.x] = at;
+      *reinterpret_cast<uint4*>(cursor + threadIdx.x * kCopies) =
+          make_uint4(at, at + n.x, at + n.x + n.y, at + n.x + n.y + n.z);
       if (threadIdx.x == kMaxWindows - 1) start[kMaxWindows] = incl;
     }
   }
   __device__ inline void place(uint32_t at, float v) const {
-    const uint32_t i = atomicAdd(&cursor[at / kSize], 1u);
+    const uint32_t i = atomicAdd(counter(at), 1u);
     val[i] = v, rel[i] = (uint16_t)(at % kSize);
   }
   __device__ inline Window<kThr> at_window(int k) const { return {window + (two ? (k & 1) * kSize : 0)}; }
