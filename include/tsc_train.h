@@ -25,7 +25,7 @@ extern "C" {
  * teacher_temperature NULL (a prefix of a support is renormalised).
  *
  * logits       [N, V] row-major, row stride ld >= V, float32 or bfloat16 (dtype). Read only.
- * N, V         0 <= N <= 2^21, 1 <= V < 2^31 - 16.
+ * N, V         0 <= N <= 2^21, 1 <= V < 2^31 - 16, and N ceil(V / 2^19) <= 2^21.
  * temperature  [N] float32, normal positive finite.
  * teacher_ids, teacher_values [N, W] int32 and float32: entries past lengths[n] are not read. Ids
  *              in [0, V); an id that occurs twice counts twice. A value of -inf has probability 0.

@@ -107,6 +107,39 @@ def test_distill_against_the_oracle(N, V, W, dtype, pad, base, tt):
     assert torch.equal(plain.loss, out.loss.detach()) and not plain.loss.requires_grad
 
 
+@pytest.mark.parametrize("N,V,W,dtype", [
+    (300, 200000, 4608, "f32"), (512, 262144, 300, "bf16"), (130, 524288, 16384, "bf16"),
+    (200, 100000, 4608, "bf16"), (127, 65537, 2048, "bf16"), (140, 524289, 64, "bf16"),
+])
+def test_one_call_agrees_with_two(N, V, W, dtype):
+    # distill_topk_grad chooses between one kernel and several by the sizes; autograd always takes
+    # the several. Each gradient is the same float32 value up to a few roundings, and rounded once:
+    # at most one step of its type (2 * HALF) apart, beside those roundings where terms cancel: of
+    # q and p each NUM + LSE(V) + a few 2^-24 of values <= 1, on both sides less than 2^-16.
+    log(f"case distill in one call and in two N={N} V={V} W={W} {dtype}")
+    g = torch.Generator(DEV).manual_seed(V)
+    x = torch.randn(N, V, device=DEV, generator=g).mul_(3).to(DT[dtype])
+    rng = np.random.default_rng(V)
+    row = tensor(rng.permutation(V)[:W], torch.int64)
+    ids = ((row[None] + torch.arange(N, device=DEV)[:, None] * 7919) % V).to(torch.int32)
+    values = torch.randn(N, W, device=DEV, generator=g)
+    lengths = torch.randint(0, W + 1, (N,), device=DEV, generator=g).to(torch.int32)
+    T = torch.rand(N, device=DEV, generator=g) + 0.5
+    w = torch.randn(N, device=DEV, generator=g)
+    one = tsc.distill_topk_grad(x, ids, values, lengths, T, w)
+    leaf = x.requires_grad_()
+    out = tsc.distill_topk(leaf, ids, values, lengths, T)
+    (grad,) = torch.autograd.grad(out.loss, leaf, w)
+    assert torch.equal(one.row_status, out.row_status)
+    loss = out.loss.detach()
+    # The loss is a difference of terms of up to about 20, its float32 roundings those of either.
+    assert torch.all((one.loss - loss).abs() <= 2 * (20 * lse_bound(V) + 2.0 ** -24 * loss.abs()))
+    for n in range(0, N, 16):
+        a, b = one.grad_logits[n : n + 16].float(), grad[n : n + 16].float()
+        scale = (w[n : n + 16].abs() / T[n : n + 16])[:, None]
+        assert torch.all((a - b).abs() <= 2 * HALF[dtype] * b.abs() * 1.01 + scale * 2.0 ** -16)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_distill_edges(dtype):
     log(f"case distill edges {dtype}")
@@ -283,6 +316,60 @@ def test_replay_gradient_against_the_oracle(N, V, W, dtype, wide, pad, base):
     rep = tsc.replay_logprob(leaf, *args, *kw.values())
     rep.selected_logprob.sum().backward()
     check_replay_grad(c, dtype, np.ones(N, np.float32), None, leaf.grad)
+
+
+@pytest.mark.parametrize("V,W,dtype,both", [
+    (2100, 2100, "f32", True), (4096, 4000, "bf16", False), (30011, 2600, "bf16", True),
+    (70001, 6000, "f32", False), (129280, 8192, "bf16", True), (520000, 16384, "bf16", False),
+    (530000, 16384, "bf16", False),
+])
+def test_replay_gradient_of_long_supports(V, W, dtype, both):
+    log(f"case replay gradient of long supports V={V} W={W} {dtype} both={both}")
+    rng = np.random.default_rng(V + W)
+    N = 5
+    c = replay_case(rng, N, V, W, dtype)
+    # The whole width, short rows and rows around it; ids next to each other, the last one of all.
+    c["lengths"][:] = (W, 2049, W - 1, 3, W)
+    ids = np.stack([rng.permutation(V)[:W] for _ in range(N)]).astype(np.int32)
+    ids[0] = np.arange(V - W, V)
+    c["ids"], c["S"] = ids, [ids[n, :m] for n, m in enumerate(c["lengths"])]
+    c["tok"] = ids[:, 1].copy()
+    c["tok"][0] = V - 1
+    xt = c["xt"]
+    xt[2, int(ids[2, W - 1])] = float("nan")  # just outside row 2's support
+    xt[4, int(ids[4, 7])] = -float("inf")
+    c["x"] = xt.double().cpu().numpy()
+    args, _ = replay_inputs(c, False)
+    gs = rng.standard_normal(N).astype(np.float32)
+    gl = rng.standard_normal((N, W)).astype(np.float32) if both else None
+    call = lambda: tsc.replay_logprob_backward(xt, *args, tensor(gs, torch.float32),
+                                               None if gl is None else tensor(gl, torch.float32))
+    check_replay_grad(c, dtype, gs, gl, call())
+    # An id out of range, and a NaN within the support: no gradient. A repeated id counts twice in
+    # the sums, as it does in the forward call, whatever the row's length.
+    c["ids"][0, W // 2] = V
+    xt[1, int(c["ids"][1, 5])] = float("nan")
+    c["ids"][4, W - 1] = c["ids"][4, 11]
+    args, _ = replay_inputs(c, False)
+    rep = tsc.replay_logprob(xt, *args, return_logprobs=True)
+    assert (rep.row_status != 0).tolist() == [True, True, False, False, False]
+    grad = call()
+    assert torch.all(grad[:2] == 0)
+    S, t = c["ids"][4], float(c["T"][4])
+    g = np.zeros(W) if gl is None else gl[4].astype(np.float64)
+    total = float(gs[4]) + g.sum()
+    z = (c["x"][4][S] - c["x"][4][S].max()) / t
+    pi = np.exp(z) / np.sum(np.exp(z))
+    want, ok = np.zeros(V), np.zeros(V)
+    np.add.at(want, S, (g - pi * total) / t)
+    want[c["tok"][4]] += float(gs[4]) / t
+    # The bounds of check_replay_grad, added up over an id's entries, and the addition.
+    np.add.at(ok, S, (pi * abs(total) * (numerator_bound(z) + lse_bound(W) + 7 * 2.0 ** -24)
+                      + np.abs(g) * 6 * 2.0 ** -24) / t)
+    ok[c["tok"][4]] += abs(gs[4]) * 6 * 2.0 ** -24 / t
+    ok += HALF[dtype] * np.abs(want) * 1.01 + 1e-40 * (want != 0)
+    off = np.abs(grad[4].double().cpu().numpy() - want)
+    assert np.all(off <= ok), (np.argmax(off - ok), off.max(), ok[np.argmax(off - ok)])
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -122,6 +122,16 @@ def test_replay_backward_checks(lib, kw, code):
     assert lib.tsc_replay_logprob_backward(*a.values()) == code
 
 
+def test_more_segments_than_a_grid_holds(lib):
+    # One workgroup per row and segment: 2^21 rows of three segments are refused, before any pointer
+    # is looked at.
+    big = dict(N=2**21, V=2**20 + 1, ld=2**20 + 1)
+    assert lib.tsc_distill_topk_backward(*distill_args(tail=BACKWARD, **big)) == 2
+    assert lib.tsc_distill_topk_grad(*distill_args(tail=BOTH, **big)) == 2
+    assert lib.tsc_replay_logprob_backward(0x1000, 1, 2**21, 2**20 + 1, 2**20 + 1, 8, 8, 8, 16, None,
+                                           None, 0, 8, None, None, 0x40, None) == 2
+
+
 def test_workspace_sizes(lib):
     for N, K, V in [(1, 0, 1), (1, 4, 151936), (64, 4, 151936), (3, 256, 2**31 - 17), (2**21, 2, 100)]:
         a, b = (lib.tsc_verify_drafts_workspace(N, K, V, d) for d in (0, 1))

@@ -118,7 +118,9 @@ int64_t distill_bytes(int64_t N, int64_t V) {
 int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld, int32_t W) {
   if (!dtype_ok(dtype) || N < 0 || V < 1 || V > kMaxVocab || ld < V || W < 1)
     return TSC_ERR_INVALID_ARGUMENT;
-  if (N > kMaxRows || W > TSC_MAX_PACKED_WIDTH) return TSC_ERR_UNSUPPORTED;
+  // One workgroup per row and segment.
+  if (N > kMaxRows || W > TSC_MAX_PACKED_WIDTH || N * ceil_div(V, tsc::kMaxSegment) > kMaxRows)
+    return TSC_ERR_UNSUPPORTED;
   if (N > 0 && (!logits || !aligned(logits, dtype))) return TSC_ERR_INVALID_ARGUMENT;
   return TSC_OK;
 }
@@ -142,15 +144,16 @@ void launch_distill_loss(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s
   }
 }
 
-// A kernel that writes gradients, with LDS for W entries.
+// A kernel that writes gradients, with LDS for W entries and no less than `least` bytes of it.
 template <int kThr, class Args>
 hipError_t launch_grad(void (*kernel)(Args), const Args& a, int64_t groups, std::atomic<uint64_t>& allowed,
-                       hipStream_t s) {
+                       hipStream_t s, size_t least = 0, int64_t more = 0) {
   using Ent = tsc::Entries<kThr>;
   static_assert(Ent::bytes(TSC_MAX_PACKED_WIDTH) <= (size_t)Ent::kAll, "the widest rows fit");
   const hipError_t err = allow_lds(kernel, (size_t)Ent::kAll, allowed);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThr), Ent::bytes(a.W), s, a);
+  const size_t need = Ent::bytes(a.W, more), bytes = need > least ? need : least;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThr), bytes, s, a);
   return hipGetLastError();
 }
 
@@ -166,11 +169,36 @@ hipError_t launch_distill_grad(const tsc::DistillArgs& a, int32_t dtype, hipStre
 // 151936 take 42 us against 48 and a launch, 1024 rows 160 against 170; 64 rows 35 against 30.)
 bool fused(int64_t N, int64_t V) { return V <= tsc::kMaxSegment && (N >= 128 || V <= 65536); }
 
+// The fused kernel's second reading of a row comes from the last-level cache (256 MB), if the rows
+// of all resident workgroups fit there. Two workgroups share a CU, 512 rows in all; past kCached
+// bytes of rows one workgroup is kept to a CU, by asking for more than half of its LDS. (bf16,
+// W = 4608, 512 rows: of 262144, 268 MB, 141 us alone against 157 in pairs; of 200000, 205 MB,
+// 116 against 123; of 151936, 156 MB, 95 against 91; 1024 rows of 32000 88 against 67.)
+constexpr int64_t kCached = 180 << 20;
+constexpr size_t kAlone = 84 * 1024;
+
 hipError_t launch_distill_fused(const tsc::DistillArgs& a, int32_t dtype, hipStream_t s) {
   static std::atomic<uint64_t> f32{0}, bf16{0};
+  const int64_t rows = (a.N < 512 ? a.N : 512) * a.V * (dtype == TSC_DTYPE_F32 ? 4 : 2);
+  const size_t least = rows > kCached ? kAlone : 0;
   return dtype == TSC_DTYPE_F32
-             ? launch_grad<tsc::kGradThreads>(&tsc::distill_fused_kernel<TSC_DTYPE_F32>, a, a.N, f32, s)
-             : launch_grad<tsc::kGradThreads>(&tsc::distill_fused_kernel<TSC_DTYPE_BF16>, a, a.N, bf16, s);
+             ? launch_grad<tsc::kGradThreads>(&tsc::distill_fused_kernel<TSC_DTYPE_F32>, a, a.N, f32, s, least)
+             : launch_grad<tsc::kGradThreads>(&tsc::distill_fused_kernel<TSC_DTYPE_BF16>, a, a.N, bf16, s, least);
+}
+
+// Packed rows of so many entries that a bitmask in LDS and two passes over the row cost less than
+// gathering them. Gathering costs a cache line per entry, the passes V / 64 lines or more each.
+// (256 rows, gathered against streamed: bf16 of 151936, 36 us against 42 for 4096 entries, 61
+// against 43 for 8192; of 32000, 15.3 against 14.6 for 2048; float32 of 100000, 57 against 56 for
+// 4096.)
+struct Dense {
+  int32_t above, mask_bytes;
+};
+Dense dense_rows(int64_t V, int32_t W) {
+  using Ent = tsc::Entries<tsc::kGradThreads>;
+  const int64_t mask = ceil_div(V, 32) * 4, above = V / 28 > 2048 ? V / 28 : 2048;
+  if (W <= above || V > tsc::kMaxSegment || Ent::bytes(W, mask) > (size_t)Ent::kAll) return {INT32_MAX, 0};
+  return {(int32_t)above, (int32_t)mask};
 }
 
 // Workspace of loss and gradient in one call: slices' states, and the rows' statistics.
@@ -353,16 +381,17 @@ int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N
       !aligned(grad_logits, dtype) || (support_bits && bits_ld < (V + 7) / 8))
     return TSC_ERR_INVALID_ARGUMENT;
   const Cut cut = grad_cut(N, V, 256);
+  const Dense dense = dense_rows(V, W);
   const tsc::ReplayGradArgs a{logits, N, V, ld, temperature, packed_ids, lengths, W, capture_status,
                               support_bits, bits_ld, tokens, grad_selected, grad_logprobs,
-                              grad_logits, cut.n, cut.len};
+                              grad_logits, cut.n, cut.len, dense.above, dense.mask_bytes};
   (void)hipGetLastError();
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   static std::atomic<uint64_t> f32{0}, bf16{0};
   const hipError_t err =
       dtype == TSC_DTYPE_F32
-          ? launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<TSC_DTYPE_F32>, a, N * cut.n, f32, s)
-          : launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<TSC_DTYPE_BF16>, a, N * cut.n, bf16, s);
+          ? launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<TSC_DTYPE_F32>, a, N * cut.n, f32, s, 0, dense.mask_bytes)
+          : launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<TSC_DTYPE_BF16>, a, N * cut.n, bf16, s, 0, dense.mask_bytes);
   return err == hipSuccess ? TSC_OK : TSC_ERR_HIP;
 }
 

@@ -27,6 +27,8 @@ struct ReplayGradArgs {
   void* grad;                    // [N, V], contiguous
   int32_t segments;
   int64_t seg_len;
+  int32_t dense;       // packed rows longer than this are streamed under a bitmask in LDS
+  int32_t mask_bytes;  // of that bitmask, for V bits; 0 where no row is that long
 };
 
 constexpr int kGradThreads = 1024;
@@ -47,33 +49,34 @@ struct ReplayShared {
   double s[kGradWaves], g[kGradWaves];
 };
 
-// Entries i0, i0 + kGradThreads, ... of a packed row: ids, upstream gradients and logits (id -1 past
-// the length).
+// Entries i0, i0 + kGradThreads, ... of a packed row: ids (-1 past the length), upstream gradients
+// and, unless the row is streamed, logits.
 template <int DT, int N>
 struct PackedEntries {
   static constexpr int kE = N;
   int32_t id[N];
   float up[N], x[N];
-  __device__ inline void load(const int32_t* ids, const float* gl, const typename Row<DT>::Bits* row, int64_t V,
-                              int32_t len, int32_t i0) {
+  __device__ inline void load(const int32_t* ids, const float* gl, const typename Row<DT>::Bits* row, bool streamed,
+                              int64_t V, int32_t len, int32_t i0) {
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       id[u] = i0 + u * kGradThreads < len ? ids[i0 + u * kGradThreads] : -1;
       up[u] = gl && i0 + u * kGradThreads < len ? gl[i0 + u * kGradThreads] : 0.0f;
     }
 #pragma unroll
-    for (int u = 0; u < N; ++u) x[u] = id[u] >= 0 && id[u] < V ? Row<DT>::get(row + id[u]) : -__builtin_inff();
+    for (int u = 0; u < N; ++u)
+      x[u] = !streamed && id[u] >= 0 && id[u] < V ? Row<DT>::get(row + id[u]) : -__builtin_inff();
   }
 };
 
 // Mask bytes and logits of a bitmask row, kAhead windows before their turn. Lanes past the last
 // whole chunk of [lo, hi) ask for the first one, and use nothing of it.
-template <int DT>
+template <int DT, class Mask>
 struct MaskedStream {
   static constexpr int kSize = Window<kGradThreads>::kSize;
   static constexpr int kAhead = DT == TSC_DTYPE_BF16 ? 4 : 2;
   const typename Row<DT>::Bits* row;
-  const uint8_t* bits;
+  Mask bits;
   int64_t lo, hi;
   typename Row<DT>::Chunk v[kAhead];
   uint32_t b[kAhead];
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
   using B = typename Row<DT>::Bits;
   extern __shared__ __attribute__((aligned(16))) float dyn_lds[];
   __shared__ ReplayShared sh;
-  const Entries<kGradThreads> ent(dyn_lds, a.W);
+  const Entries<kGradThreads> ent(dyn_lds, a.W, a.mask_bytes);
   const int64_t n = blockIdx.x / a.segments;
   const int64_t lo = (blockIdx.x - n * a.segments) * a.seg_len;
   const int64_t hi = lo + a.seg_len < a.V ? lo + a.seg_len : a.V;
@@ -140,12 +143,42 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
   const uint8_t* bits = from_bits ? a.bits + n * a.bits_ld : nullptr;
   const int32_t* ids = a.ids + n * a.W;
   const float* gl = a.grad_logprobs ? a.grad_logprobs + n * a.W : nullptr;
-  const bool entries = !from_bits || (gl != nullptr && len_ok);  // the packed ids take part
 
-  // Entries of the packed row: a thread's first kFirst stay in registers, the rest come kMore at a
-  // time, all of their loads together, and are read again when they are placed.
-  constexpr int kFirst = 2, kMore = 6;
+  uint32_t flags = 0;  // 1: an id out of range, 2: an element of the support, 4: the token is one
+  // A long packed row is turned into a bitmask in LDS and treated as a bitmask row, unless an id
+  // occurs twice.
+  uint32_t* own = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(dyn_lds) +
+                                              Entries<kGradThreads>::bytes(a.W, a.mask_bytes) - a.mask_bytes);
+  bool streamed = from_bits;
+  if (!from_bits && len > a.dense) {
+    for (int32_t i = tid; i < a.mask_bytes / 4; i += kGradThreads) own[i] = 0u;
+    lds_barrier();
+    uint32_t again = 0u;
+    constexpr int kU = 8;
+    for (int32_t i0 = tid; i0 - tid < len; i0 += kU * kGradThreads) {
+      int32_t id[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) id[u] = i0 + u * kGradThreads < len ? ids[i0 + u * kGradThreads] : INT32_MIN;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t bit = 1u << (id[u] & 31);
+        if (id[u] >= 0 && id[u] < a.V)
+          again |= atomicOr(own + (id[u] >> 5), bit) & bit;
+        else if (id[u] != INT32_MIN || i0 + u * kGradThreads < len)
+          flags |= 1u;
+      }
+    }
+    streamed = block_all<kGradWaves>(again, [](uint32_t p, uint32_t q) { return p | q; }, sh.f) == 0u;
+  }
+  const bool entries = !streamed || (gl != nullptr && len_ok);  // the packed ids take part
+
+  // Entries of the packed row: a thread's first kKept stay in registers (longer rows' second half
+  // of them is skipped as a whole where there is none), the rest come kMore at a time, all of their
+  // loads together, and are read again when they are placed.
+  constexpr int kFirst = 2, kKept = 4, kMore = 4;
   PackedEntries<DT, kFirst> first;
+  PackedEntries<DT, kKept - kFirst> second;
+  const bool longer = entries && len > kFirst * kGradThreads;
   // Whether entry u is of the support and, if so, of this segment.
   auto of_support = [&](int32_t id) {
     return id >= 0 && id < a.V && (!from_bits || ((bits[id >> 3] >> (id & 7)) & 1u));
@@ -153,31 +186,32 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
   auto here = [&](int32_t id) { return id >= lo && id < hi && of_support(id); };
   LseState st;
   double G = 0.0;
-  uint32_t flags = 0;  // 1: an id out of range, 2: an element of the support, 4: the token is one
-  if (entries) first.load(ids, gl, row, a.V, len, tid);
+  if (entries) first.load(ids, gl, row, streamed, a.V, len, tid);
+  if (longer) second.load(ids, gl, row, streamed, a.V, len, tid + kFirst * kGradThreads);
   ent.begin();
   lds_barrier();
   auto look = [&](auto& t, int32_t i0) {
-    if (!from_bits) st.add(t.x, c);
+    if (!streamed) st.add(t.x, c);
 #pragma unroll
     for (int u = 0; u < t.kE; ++u) {
       const int32_t id = t.id[u];
-      if (!from_bits && i0 + u * kGradThreads < len) flags |= id < 0 || id >= a.V ? 1u : id == tok ? 6u : 2u;
+      if (!streamed && i0 + u * kGradThreads < len) flags |= id < 0 || id >= a.V ? 1u : id == tok ? 6u : 2u;
       if (of_support(id)) G += (double)t.up[u];
       if (here(id)) ent.count((uint32_t)(id - lo));
     }
   };
   if (entries) {
     look(first, tid);
-    for (int32_t i0 = tid + kFirst * kGradThreads; i0 - tid < len; i0 += kMore * kGradThreads) {
+    if (longer) look(second, tid + kFirst * kGradThreads);
+    for (int32_t i0 = tid + kKept * kGradThreads; i0 - tid < len; i0 += kMore * kGradThreads) {
       PackedEntries<DT, kMore> t;
-      t.load(ids, gl, row, a.V, len, i0);
+      t.load(ids, gl, row, streamed, a.V, len, i0);
       look(t, i0);
     }
   }
-  if (from_bits) {
-    // The whole row and its mask are streamed: where members are so many that they did not fit
-    // the packed width, hardly a line of the row is without one.
+  // The whole row and its mask are streamed: where members are so many, hardly a line of the row is
+  // without one.
+  auto stream_stats = [&](auto mask) {
     constexpr int kU = DT == TSC_DTYPE_BF16 ? 4 : 2;  // chunks of a thread at a time, and as many ahead
     constexpr int64_t kStep = kGradThreads * 8;
     const int64_t whole = a.V & ~int64_t{7}, start = (int64_t)tid * 8;
@@ -185,7 +219,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
     uint32_t b[kU], any = 0;
     auto ask = [&](int u, int64_t at) {  // past the last whole chunk: the first one, without members
       const bool in = at < whole;
-      b[u] = bits[in ? at >> 3 : 0];
+      b[u] = mask[in ? at >> 3 : 0];
       v[u] = Row<DT>::load(row + (in ? at : 0));
       if (!in) b[u] = 0u;
     };
@@ -209,7 +243,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
       st.add(f, c);
     }
     if (whole < a.V && tid == 0) {  // the ragged last chunk
-      const uint32_t last = bits[whole >> 3] & ((1u << (a.V & 7)) - 1u);
+      const uint32_t last = mask[whole >> 3] & ((1u << (a.V & 7)) - 1u);
       float f[8];
       load8<DT>(row, whole, a.V, f);
 #pragma unroll
@@ -218,8 +252,12 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
       st.add(f, c);
       any |= last;
     }
-    flags |= (any != 0u ? 2u : 0u) | ((bits[tok >> 3] >> (tok & 7)) & 1u ? 4u : 0u);
-  }
+    flags |= (any != 0u ? 2u : 0u) | ((mask[tok >> 3] >> (tok & 7)) & 1u ? 4u : 0u);
+  };
+  if (from_bits)
+    stream_stats(bits);
+  else if (streamed)
+    stream_stats(reinterpret_cast<const uint8_t*>(own));
   // The workgroup's maximum and flags, then its sums; between the two barriers the first wave
   // also turns the windows' counts into offsets.
   const float wm = wave_max(st.m);
@@ -247,20 +285,21 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
   G += (double)gs;
   const float inv_T = 1.0f / T;
   const float share = (float)(G / ((double)T * S));  // sum of G over T s
-  // What a packed id adds: all of a packed row's gradient, the upstream gradient alone of a
-  // bitmask row's, whose other term comes with the stream.
+  // What a packed id adds: all of the gradient, or the upstream gradient alone where the other term
+  // comes with the stream.
   auto place = [&](const auto& t) {
 #pragma unroll
     for (int u = 0; u < t.kE; ++u)
       if (here(t.id[u]))
         ent.place((uint32_t)(t.id[u] - lo),
-                  t.up[u] * inv_T - (from_bits ? 0.0f : exp2_scaled(t.x[u] - m, c) * share));
+                  t.up[u] * inv_T - (streamed ? 0.0f : exp2_scaled(t.x[u] - m, c) * share));
   };
   if (entries) {
     place(first);
-    for (int32_t i0 = tid + kFirst * kGradThreads; i0 - tid < len; i0 += kMore * kGradThreads) {
+    if (longer) place(second);
+    for (int32_t i0 = tid + kKept * kGradThreads; i0 - tid < len; i0 += kMore * kGradThreads) {
       PackedEntries<DT, kMore> t;
-      t.load(ids, gl, row, a.V, len, i0);
+      t.load(ids, gl, row, streamed, a.V, len, i0);
       place(t);
     }
   }
@@ -275,7 +314,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
     add(0);
     lds_barrier();
   }
-  if (!from_bits) {
+  if (!streamed) {
     for (int k = 0; lo + (int64_t)k * kSize < hi; ++k) {
       ent.turn(k, add, [&] {
         const int64_t at = lo + (int64_t)k * kSize + tid * 8;
@@ -295,27 +334,33 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
                              member_mask(b, e));
     store8<DT>(out, at, hi, r);
   };
-  MaskedStream<DT> stream{row, bits, lo, hi};
-  if (entries) {
-    stream.run([&](int k, int64_t at, float (&v)[8], uint32_t b) {
-      ent.turn(k, add, [&] {
+  auto write_row = [&](auto mask) {
+    MaskedStream<DT, decltype(mask)> stream{row, mask, lo, hi};
+    if (entries) {
+      stream.run([&](int k, int64_t at, float (&v)[8], uint32_t b) {
+        ent.turn(k, add, [&] {
+          if (at >= hi) return;
+          float r[8];
+          ent.at_window(k).take(tid, r);
+          write(at, v, b, r);
+        });
+      });
+    } else {  // the token alone has an upstream gradient: no windows, no barriers
+      stream.run([&](int, int64_t at, float (&v)[8], uint32_t b) {
         if (at >= hi) return;
-        float r[8];
-        ent.at_window(k).take(tid, r);
+        float r[8] = {};
+        if (at >> 3 == tok >> 3) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[e] = e == (tok & 7) ? gs * inv_T : 0.0f;
+        }
         write(at, v, b, r);
       });
-    });
-  } else {  // the token alone has an upstream gradient: no windows, no barriers
-    stream.run([&](int, int64_t at, float (&v)[8], uint32_t b) {
-      if (at >= hi) return;
-      float r[8] = {};
-      if (at >> 3 == tok >> 3) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = e == (tok & 7) ? gs * inv_T : 0.0f;
-      }
-      write(at, v, b, r);
-    });
-  }
+    }
+  };
+  if (from_bits)
+    write_row(bits);
+  else
+    write_row(reinterpret_cast<const uint8_t*>(own));
 }
 
 }  // namespace tsc

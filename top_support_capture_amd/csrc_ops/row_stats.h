@@ -289,12 +289,15 @@ struct Entries {
   __host__ __device__ static constexpr int64_t with(int windows, int64_t W) {
     return windows * kSize * 4 + W * 4 + kFixed + (W + 1) / 2 * 4;
   }
-  __host__ __device__ static constexpr bool takes_two(int64_t W) {
-    return with(2, W) <= (with(1, W) <= kHalf ? kHalf : kAll);
+  // `more`: bytes that the kernel needs behind them.
+  __host__ __device__ static constexpr bool takes_two(int64_t W, int64_t more) {
+    return with(2, W) + more <= (with(1, W) + more <= kHalf ? kHalf : kAll);
   }
-  __host__ __device__ static constexpr size_t bytes(int64_t W) { return (size_t)with(takes_two(W) ? 2 : 1, W); }
-  __device__ inline explicit Entries(void* lds, int32_t W) {
-    two = takes_two(W);
+  __host__ __device__ static constexpr size_t bytes(int64_t W, int64_t more = 0) {
+    return (size_t)(with(takes_two(W, more) ? 2 : 1, W) + more);
+  }
+  __device__ inline explicit Entries(void* lds, int32_t W, int64_t more = 0) {
+    two = takes_two(W, more);
     window = reinterpret_cast<float*>(lds);
     start = reinterpret_cast<uint32_t*>(window + (two ? 2 : 1) * kSize);
     cursor = start + kMaxWindows + 4;  // 16-byte aligned, as `lds` and the window's size are
