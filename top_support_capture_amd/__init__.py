@@ -297,15 +297,18 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
 
     Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``);
     with ``stream`` given, their backward pass runs there too."""
+    args = (logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
+            return_logprobs)
     if torch.is_grad_enabled() and logits.requires_grad:
-        def call():
-            return replay_logprob(logits.detach(), temperature, packed_ids, lengths, tokens,
-                                  capture_status, support_bits, return_logprobs)
-        args = (call, logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits)
         if stream is None:
             return ReplayOutput(*ReplayGradient.apply(*args))
         with torch.cuda.stream(stream):
             return ReplayOutput(*ReplayGradient.apply(*args))
+    return _replay_forward(*args, stream)
+
+
+def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
+                    return_logprobs, stream=None) -> ReplayOutput:
     lib = library()
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [N, V] with unit column stride")
@@ -335,12 +338,15 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
                        torch.empty((N, W), dtype=torch.float32, device=dev)
                        if return_logprobs else None,
                        torch.empty(N, dtype=torch.int8, device=dev))
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if stream is None and dev.type == "cuda":
+        s = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        s = (stream or torch.cuda.current_stream(dev)).cuda_stream
     code = lib.tsc_replay_logprob(logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(),
                                   packed_ids.data_ptr(), lengths.data_ptr(), W,
                                   _ptr(capture_status), _ptr(support_bits), bits_ld,
                                   tokens.data_ptr(), out.selected_logprob.data_ptr(),
-                                  _ptr(out.logprobs), out.row_status.data_ptr(), s.cuda_stream)
+                                  _ptr(out.logprobs), out.row_status.data_ptr(), s)
     if code != 0:
         raise TscError(code, lib.tsc_status_string(code).decode())
     return out

@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import TscError, _check, _launch, _logits_dtype, _ptr, library
+from . import TscError, _check, _launch, _logits_dtype, _ptr, _replay_forward, library
 
 __all__ = ["distill_topk", "DistillOutput", "distill_topk_grad", "DistillGradOutput",
            "replay_logprob_backward"]
@@ -59,13 +59,15 @@ def _distill_args(logits, teacher_ids, teacher_values, lengths, temperature, tea
     _check(temperature, "temperature", torch.float32, N, dev)
     if teacher_temperature is not None:
         _check(teacher_temperature, "teacher_temperature", torch.float32, N, dev)
-    if torch.is_grad_enabled() and (
-            teacher_values.requires_grad or temperature.requires_grad
+    return (logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), teacher_ids.data_ptr(),
+            teacher_values.data_ptr(), lengths.data_ptr(), W, _ptr(teacher_temperature)), dev
+
+
+def _refuse_other_gradients(teacher_values, temperature, teacher_temperature) -> None:
+    if (teacher_values.requires_grad or temperature.requires_grad
             or (teacher_temperature is not None and teacher_temperature.requires_grad)):
         raise ValueError("the distillation has no gradient with respect to teacher_values, "
                          "temperature or teacher_temperature: detach them")
-    return (logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), teacher_ids.data_ptr(),
-            teacher_values.data_ptr(), lengths.data_ptr(), W, _ptr(teacher_temperature)), dev
 
 
 def _distill_forward(logits, teacher_ids, teacher_values, lengths, temperature,
@@ -144,12 +146,13 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     when the weights are known beforehand, ``distill_topk_grad`` gives loss and gradient in one
     call."""
     args = (logits, teacher_ids, teacher_values, lengths, temperature, teacher_temperature)
-    if torch.is_grad_enabled() and logits.requires_grad:
-        _distill_args(*args)
-        if stream is None:
-            return DistillOutput(*_Distill.apply(*args))
-        with torch.cuda.stream(stream):  # the backward pass runs there too
-            return DistillOutput(*_Distill.apply(*args))
+    if torch.is_grad_enabled():
+        _refuse_other_gradients(teacher_values, temperature, teacher_temperature)
+        if logits.requires_grad:
+            if stream is None:
+                return DistillOutput(*_Distill.apply(*args))
+            with torch.cuda.stream(stream):  # the backward pass runs there too
+                return DistillOutput(*_Distill.apply(*args))
     loss, status, _ = _distill_forward(*args, stream)
     return DistillOutput(loss, status)
 
@@ -162,25 +165,24 @@ def distill_topk_grad(logits: torch.Tensor, teacher_ids: torch.Tensor,
     """The losses of ``distill_topk`` and the gradient of sum(row_weights * loss) with respect to
     ``logits``, in one call and without autograd. ``row_weights``: float32 [N]."""
     lib = library()
-    with torch.no_grad():
-        args, dev = _distill_args(logits, teacher_ids, teacher_values, lengths, temperature,
-                                  teacher_temperature)
-        N, V = logits.shape
-        _check(row_weights, "row_weights", torch.float32, N, dev)
-        nbytes = lib.tsc_distill_topk_grad_workspace(N, V)
+    args, dev = _distill_args(logits, teacher_ids, teacher_values, lengths, temperature,
+                              teacher_temperature)
+    N, V = logits.shape
+    _check(row_weights, "row_weights", torch.float32, N, dev)
+    nbytes = lib.tsc_distill_topk_grad_workspace(N, V)
 
-        def go(s):
-            out = DistillGradOutput(torch.empty(N, dtype=torch.float32, device=dev),
-                                    torch.empty((N, V), dtype=logits.dtype, device=dev),
-                                    torch.empty(N, dtype=torch.int8, device=dev))
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            code = lib.tsc_distill_topk_grad(*args, row_weights.data_ptr(), out.loss.data_ptr(),
-                                             out.row_status.data_ptr(), out.grad_logits.data_ptr(),
-                                             ws.data_ptr(), nbytes, s)
-            _raise(lib, code, "tsc_distill_topk_grad")
-            return out
+    def go(s):
+        out = DistillGradOutput(torch.empty(N, dtype=torch.float32, device=dev),
+                                torch.empty((N, V), dtype=logits.dtype, device=dev),
+                                torch.empty(N, dtype=torch.int8, device=dev))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        code = lib.tsc_distill_topk_grad(*args, row_weights.data_ptr(), out.loss.data_ptr(),
+                                         out.row_status.data_ptr(), out.grad_logits.data_ptr(),
+                                         ws.data_ptr(), nbytes, s)
+        _raise(lib, code, "tsc_distill_topk_grad")
+        return out
 
-        return _launch(dev, stream, go)
+    return _launch(dev, stream, go)
 
 
 def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
@@ -229,19 +231,20 @@ def _replay_backward(ctx, grad_selected, grad_logprobs):
         logits, T, ids, lengths, tokens,
         None if grad_selected is None else grad_selected.contiguous(),
         None if grad_logprobs is None else grad_logprobs.contiguous(), status, bits)
-    return (None, grad) + (None,) * 6
+    return (grad,) + (None,) * 7
 
 
 _replay_backward_once = once_differentiable(_replay_backward)
 
 
 class ReplayGradient(torch.autograd.Function):
-    """``replay_logprob`` with its gradient; ``call`` is the forward call on the same arguments."""
+    """``replay_logprob`` with its gradient."""
 
     @staticmethod
-    def forward(ctx, call, logits, temperature, packed_ids, lengths, tokens, capture_status,
-                support_bits):
-        out = call()
+    def forward(ctx, logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
+                return_logprobs):
+        out = _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_status,
+                              support_bits, return_logprobs)
         ctx.save_for_backward(logits, temperature, packed_ids, lengths, tokens, capture_status,
                               support_bits)
         ctx.mark_non_differentiable(out.row_status)
