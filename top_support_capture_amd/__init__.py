@@ -309,6 +309,10 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
 
 def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
                     return_logprobs, stream=None) -> ReplayOutput:
+    if stream is None and logits.is_cuda and logits.device.index != torch.cuda.current_device():
+        with torch.cuda.device(logits.device):
+            return _replay_forward(logits, temperature, packed_ids, lengths, tokens,
+                                   capture_status, support_bits, return_logprobs)
     lib = library()
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [N, V] with unit column stride")
