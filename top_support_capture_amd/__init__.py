@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
 import torch  # must come first: the library binds to the HIP runtime PyTorch has loaded
@@ -153,6 +154,10 @@ def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], go):
         return go(torch._C._cuda_getCurrentRawStream(dev.index))
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         return go(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _on(stream: Optional[torch.cuda.Stream]):
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(t: torch.Tensor, name: str, dtype, n: int, dev) -> None:
@@ -297,14 +302,11 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
 
     Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``);
     with ``stream`` given, their backward pass runs there too."""
-    args = (logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
-            return_logprobs)
-    if torch.is_grad_enabled() and logits.requires_grad:
-        if stream is None:
-            return ReplayOutput(*ReplayGradient.apply(*args))
-        with torch.cuda.stream(stream):
-            return ReplayOutput(*ReplayGradient.apply(*args))
-    return _replay_forward(*args, stream)
+    others = (temperature, packed_ids, lengths, tokens, capture_status, support_bits)
+    out = _replay_forward(logits, *others, return_logprobs, stream)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return differentiable_replay(out, logits, others, stream)
+    return out
 
 
 def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
@@ -394,7 +396,7 @@ def csr_to_host(csr: SupportCsr, stream: Optional[torch.cuda.Stream] = None):
     return offsets.numpy(), ids, lps
 
 
-from .train import (DistillGradOutput, DistillOutput, ReplayGradient, distill_topk,  # noqa: E402
+from .train import (DistillGradOutput, DistillOutput, differentiable_replay, distill_topk,  # noqa: E402
                     distill_topk_grad, replay_logprob_backward)
 from .verify import (MAX_DRAFTS, Support, VerifyOutput, support_of, verify_captured,  # noqa: E402
                      verify_drafts)

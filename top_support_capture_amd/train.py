@@ -1,7 +1,7 @@
 """Training over captured supports: bindings of ``include/tsc_train.h``.
 
 ``distill_topk`` is differentiable with respect to the student's logits, and so is
-``replay_logprob`` through ``ReplayGradient``. The backward passes run on the stream that the
+``replay_logprob``. The backward passes run on the stream that the
 forward ran on, allocate the gradient, and synchronise nothing."""
 from __future__ import annotations
 
@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import TscError, _check, _launch, _logits_dtype, _ptr, _replay_forward, library
+from . import TscError, _check, _launch, _logits_dtype, _on, _ptr, library
 
 __all__ = ["distill_topk", "DistillOutput", "distill_topk_grad", "DistillGradOutput",
            "replay_logprob_backward"]
@@ -91,20 +91,36 @@ def _distill_forward(logits, teacher_ids, teacher_values, lengths, temperature,
     return _launch(dev, stream, go)
 
 
+def _whole(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return t if t is None or t.is_contiguous() else t.contiguous()
+
+
+def _saved_rows(logits: torch.Tensor):
+    """Saved logits and their row stride. What was saved was checked; what comes back has its values
+    but, through hooks on saved tensors, may be laid out anew."""
+    N, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        logits = logits.contiguous()
+    return logits, N, V, (logits.stride(0) if N > 1 else V)
+
+
 def _distill_backward(ctx, grad_loss):
-    logits, ids, values, lengths, T, teacher_T, stats = ctx.saved_tensors
+    logits, *rest = ctx.saved_tensors
+    logits, N, V, ld = _saved_rows(logits)
+    ids, values, lengths, T, teacher_T, stats = map(_whole, rest)
     lib = library()
-    args, dev = _distill_args(logits, ids, values, lengths, T, teacher_T)
 
     def go(s):
         g = grad_loss.contiguous()
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        code = lib.tsc_distill_topk_backward(*args, stats.data_ptr(), g.data_ptr(),
-                                             grad.data_ptr(), s)
+        grad = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
+        code = lib.tsc_distill_topk_backward(
+            logits.data_ptr(), _logits_dtype(logits, "logits"), N, V, ld, T.data_ptr(), ids.data_ptr(),
+            values.data_ptr(), lengths.data_ptr(), ids.shape[1], _ptr(teacher_T), stats.data_ptr(),
+            g.data_ptr(), grad.data_ptr(), s)
         _raise(lib, code, "tsc_distill_topk_backward")
         return grad
 
-    return (_launch(dev, None, go),) + (None,) * 5
+    return _launch(logits.device, None, go), None, None
 
 
 # Backward passes run without a graph unless one is asked for (create_graph); the gradient has no
@@ -113,21 +129,20 @@ _distill_backward_once = once_differentiable(_distill_backward)
 
 
 class _Distill(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, teacher_ids, teacher_values, lengths, temperature,
-                teacher_temperature):
-        loss, status, stats = _distill_forward(logits, teacher_ids, teacher_values, lengths,
-                                               temperature, teacher_temperature, None)
-        ctx.save_for_backward(logits, teacher_ids, teacher_values, lengths, temperature,
-                              teacher_temperature, stats)
-        ctx.mark_non_differentiable(status)
-        ctx.set_materialize_grads(False)
-        return loss, status
+    """The loss that a forward call has computed, as a function of the logits. The call's other
+    arguments and its results come in tuples: nothing flows back to them."""
 
     @staticmethod
-    def backward(ctx, grad_loss, _):
+    def forward(ctx, logits, others, results):
+        loss, stats = results
+        ctx.save_for_backward(logits, *others, stats)
+        ctx.set_materialize_grads(False)
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad_loss):
         if grad_loss is None:
-            return (None,) * 6
+            return None, None, None
         go = _distill_backward_once if torch.is_grad_enabled() else _distill_backward
         return go(ctx, grad_loss)
 
@@ -145,15 +160,13 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     The loss is differentiable with respect to ``logits``. Weight or average the rows with torch;
     when the weights are known beforehand, ``distill_topk_grad`` gives loss and gradient in one
     call."""
-    args = (logits, teacher_ids, teacher_values, lengths, temperature, teacher_temperature)
     if torch.is_grad_enabled():
         _refuse_other_gradients(teacher_values, temperature, teacher_temperature)
-        if logits.requires_grad:
-            if stream is None:
-                return DistillOutput(*_Distill.apply(*args))
-            with torch.cuda.stream(stream):  # the backward pass runs there too
-                return DistillOutput(*_Distill.apply(*args))
-    loss, status, _ = _distill_forward(*args, stream)
+    others = (teacher_ids, teacher_values, lengths, temperature, teacher_temperature)
+    loss, status, stats = _distill_forward(logits, *others, stream)
+    if logits.requires_grad and torch.is_grad_enabled():
+        with _on(stream):  # the backward pass runs there too
+            loss = _Distill.apply(logits, others, (loss, stats))
     return DistillOutput(loss, status)
 
 
@@ -197,7 +210,6 @@ def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
     upstream gradients of its ``selected_logprob`` and ``logprobs`` (None: 0; entries past each
     length are not read). Rows whose replay status is not ROW_OK have gradient 0. This is the
     call that autograd makes; made directly it needs no graph of torch's."""
-    lib = library()
     dt, N, V, ld, dev = _rows(logits)
     W = _packed(packed_ids, "packed_ids", torch.int32, N, None, dev)
     _check(temperature, "temperature", torch.float32, N, dev)
@@ -209,51 +221,62 @@ def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
         _packed(grad_logprobs, "grad_logprobs", torch.float32, N, W, dev)
     if capture_status is not None:
         _check(capture_status, "capture_status", torch.int8, N, dev)
-    bits_ld = 0
     if support_bits is not None:
-        bits_ld = _packed(support_bits, "support_bits", torch.uint8, N, None, dev)
+        _packed(support_bits, "support_bits", torch.uint8, N, None, dev)
 
-    def go(s):
-        grad = torch.empty((N, V), dtype=logits.dtype, device=dev)
-        code = lib.tsc_replay_logprob_backward(
-            logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), packed_ids.data_ptr(),
-            lengths.data_ptr(), W, _ptr(capture_status), _ptr(support_bits), bits_ld,
-            tokens.data_ptr(), _ptr(grad_selected), _ptr(grad_logprobs), grad.data_ptr(), s)
-        _raise(lib, code, "tsc_replay_logprob_backward")
-        return grad
+    return _launch(dev, stream, lambda s: _replay_backward_call(
+        s, logits, dt, N, V, ld, temperature, packed_ids, lengths, tokens, grad_selected,
+        grad_logprobs, capture_status, support_bits))
 
-    return _launch(dev, stream, go)
+
+def _replay_backward_call(s, logits, dt, N, V, ld, temperature, packed_ids, lengths, tokens,
+                          grad_selected, grad_logprobs, capture_status, support_bits) -> torch.Tensor:
+    lib = library()
+    grad = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
+    code = lib.tsc_replay_logprob_backward(
+        logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(), packed_ids.data_ptr(),
+        lengths.data_ptr(), packed_ids.shape[1], _ptr(capture_status), _ptr(support_bits),
+        0 if support_bits is None else support_bits.shape[1], tokens.data_ptr(), _ptr(grad_selected),
+        _ptr(grad_logprobs), grad.data_ptr(), s)
+    _raise(lib, code, "tsc_replay_logprob_backward")
+    return grad
 
 
 def _replay_backward(ctx, grad_selected, grad_logprobs):
-    logits, T, ids, lengths, tokens, status, bits = ctx.saved_tensors
-    grad = replay_logprob_backward(
-        logits, T, ids, lengths, tokens,
-        None if grad_selected is None else grad_selected.contiguous(),
-        None if grad_logprobs is None else grad_logprobs.contiguous(), status, bits)
-    return (grad,) + (None,) * 7
+    logits, *rest = ctx.saved_tensors
+    logits, N, V, ld = _saved_rows(logits)
+    T, ids, lengths, tokens, status, bits = map(_whole, rest)
+    return _launch(logits.device, None, lambda s: _replay_backward_call(
+        s, logits, _logits_dtype(logits, "logits"), N, V, ld, T, ids, lengths, tokens,
+        _whole(grad_selected), _whole(grad_logprobs), status, bits)), None, None
 
 
 _replay_backward_once = once_differentiable(_replay_backward)
 
 
-class ReplayGradient(torch.autograd.Function):
-    """``replay_logprob`` with its gradient."""
+class _Replay(torch.autograd.Function):
+    """The selected logprobs (and those of the supports) that the forward call ``out`` holds, as
+    functions of the logits; the other arguments of that call come in a tuple."""
 
     @staticmethod
-    def forward(ctx, logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
-                return_logprobs):
-        out = _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_status,
-                              support_bits, return_logprobs)
-        ctx.save_for_backward(logits, temperature, packed_ids, lengths, tokens, capture_status,
-                              support_bits)
-        ctx.mark_non_differentiable(out.row_status)
+    def forward(ctx, logits, others, out):
+        ctx.save_for_backward(logits, *others)
         ctx.set_materialize_grads(False)
-        return out.selected_logprob, out.logprobs, out.row_status
+        return out.selected_logprob if out.logprobs is None else (out.selected_logprob, out.logprobs)
 
     @staticmethod
-    def backward(ctx, grad_selected, grad_logprobs, _):
+    def backward(ctx, grad_selected, grad_logprobs=None):
         if grad_selected is None and grad_logprobs is None:
-            return (None,) * 8
+            return None, None, None
         go = _replay_backward_once if torch.is_grad_enabled() else _replay_backward
         return go(ctx, grad_selected, grad_logprobs)
+
+
+def differentiable_replay(out, logits, others, stream):
+    """``out`` of a replay with its logprobs as functions of ``logits``; their backward pass runs on
+    ``stream``."""
+    with _on(stream):
+        got = _Replay.apply(logits, others, out)
+    if out.logprobs is None:
+        return out._replace(selected_logprob=got)
+    return out._replace(selected_logprob=got[0], logprobs=got[1])
