@@ -418,6 +418,35 @@ def test_replay_gradient_edges(dtype):
     check_replay_grad(c, dtype, gs, None, grad, zero | {18})
 
 
+def test_saved_tensors_that_were_moved():
+    log("case gradients with saved tensors kept on the host; the replay on another stream")
+    rng = np.random.default_rng(31)
+    N, V, W = 4, 1003, 40
+    c = replay_case(rng, N, V, W, "f32", pad=5, base=1)
+    args, _ = replay_inputs(c, False)
+    values = tensor(rng.standard_normal((N, W)), torch.float32)
+    gs, gl = tensor(rng.standard_normal(N), torch.float32), tensor(rng.standard_normal((N, W)), torch.float32)
+
+    def grads(stream=None):
+        leaf = c["xt"].detach().requires_grad_()
+        loss = tsc.distill_topk(leaf, args[1], values, args[2], args[0], stream=stream).loss
+        rep = tsc.replay_logprob(leaf, *args, return_logprobs=True, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        return [torch.autograd.grad(loss, leaf, gs)[0],
+                torch.autograd.grad([rep.selected_logprob, rep.logprobs], leaf, [gs, gl])[0]]
+
+    want = grads()
+    with torch.autograd.graph.save_on_cpu():  # they come back contiguous: other strides
+        again = grads()
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    again = grads(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
 def test_gradients_in_a_graph():
     log("case gradients in a captured graph")
     rng = np.random.default_rng(19)
