@@ -3,8 +3,12 @@
 // selected logprob's joins its token's) give
 //     dx_j = (G_j - pi_j sum_{i in S} G_i) / T for j in S, and 0 elsewhere.
 // A workgroup writes a segment of a row (the whole row when there are rows enough). It takes the
-// support's statistics itself, which costs a gather of S (or a pass over a bitmask row) per
-// segment but no second launch; then it writes its segment once, window by window.
+// support's statistics itself, which costs a gather of S per segment (or a pass over the row, where
+// it is streamed under a bitmask) but no second launch; then it writes its segment once.
+//
+// Measured for bfloat16: 256 rows of 151936 with supports of up to 2048 take 23 us, 78 MB written
+// and 27 MB of gathered lines; 256 rows of 129280, three in four of them bitmask rows of about 10000
+// members, 37 us (195 MB: two readings and a write). 1024 rows of 151936 with 2048 entries 110 us.
 #pragma once
 
 #include "row_stats.h"
@@ -117,8 +121,11 @@ struct MaskedStream {
 // All ones where bit e of b is set: members are kept by masks, not by branches.
 __device__ inline uint32_t member_mask(uint32_t b, int e) { return (uint32_t)((int32_t)(b << (31 - e)) >> 31); }
 
-template <int DT>
-__global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGradArgs a) {
+// kStreams: rows may be streamed under a bitmask. Calls without bitmasks or rows that long take the
+// kernel without that code, which fits two workgroups to a CU (1024 rows of 32000 32 us against 44,
+// 300 of 151936 37 against 47; with the code in, the registers of two workgroups spill).
+template <int DT, bool kStreams>
+__global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_kernel(ReplayGradArgs a) {
   using B = typename Row<DT>::Bits;
   extern __shared__ __attribute__((aligned(16))) float dyn_lds[];
   __shared__ ReplayShared sh;
@@ -149,8 +156,8 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
   // occurs twice.
   uint32_t* own = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(dyn_lds) +
                                               Entries<kGradThreads>::bytes(a.W, a.mask_bytes) - a.mask_bytes);
-  bool streamed = from_bits;
-  if (!from_bits && len > a.dense) {
+  bool streamed = kStreams && from_bits;
+  if (kStreams && !from_bits && len > a.dense) {
     for (int32_t i = tid; i < a.mask_bytes / 4; i += kGradThreads) own[i] = 0u;
     lds_barrier();
     uint32_t again = 0u;
@@ -254,10 +261,12 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
     }
     flags |= (any != 0u ? 2u : 0u) | ((mask[tok >> 3] >> (tok & 7)) & 1u ? 4u : 0u);
   };
-  if (from_bits)
-    stream_stats(bits);
-  else if (streamed)
-    stream_stats(reinterpret_cast<const uint8_t*>(own));
+  if constexpr (kStreams) {
+    if (from_bits)
+      stream_stats(bits);
+    else if (streamed)
+      stream_stats(reinterpret_cast<const uint8_t*>(own));
+  }
   // The workgroup's maximum and flags, then its sums; between the two barriers the first wave
   // also turns the windows' counts into offsets.
   const float wm = wave_max(st.m);
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
     add(0);
     lds_barrier();
   }
-  if (!streamed) {
+  if (!kStreams || !streamed) {
     for (int k = 0; lo + (int64_t)k * kSize < hi; ++k) {
       ent.turn(k, add, [&] {
         const int64_t at = lo + (int64_t)k * kSize + tid * 8;
@@ -357,10 +366,12 @@ __global__ void __launch_bounds__(kGradThreads, 4) replay_grad_kernel(ReplayGrad
       });
     }
   };
-  if (from_bits)
-    write_row(bits);
-  else
-    write_row(reinterpret_cast<const uint8_t*>(own));
+  if constexpr (kStreams) {
+    if (from_bits)
+      write_row(bits);
+    else
+      write_row(reinterpret_cast<const uint8_t*>(own));
+  }
 }
 
 }  // namespace tsc

@@ -61,7 +61,9 @@ __device__ inline RacePart better(RacePart a, RacePart b) {
 }
 
 // Softmax statistics of each row's slices; greedy requests take the maximum's place of each
-// target row instead and read no draft row.
+// target row instead and read no draft row. Bound by HBM: 64 requests of 4 drafts over 151936
+// bfloat16 logits, 175 MB, take 36 us (4.8 TB/s); 4 to 8 waves a SIMD, slices of 16384 to 100000
+// elements and fewer vector instructions all measure the same. (One request: 4.3 us.)
 template <int TD, int DD>
 __global__ void __launch_bounds__(kOpThreads) verify_stats_kernel(VerifyArgs a) {
   __shared__ float sh_m[kOpWaves];
@@ -232,6 +234,10 @@ __device__ inline Decision first_stop(const int32_t* code, int32_t count, int32_
   return {stop, code[stop]};
 }
 
+// The race at the position where a request stops. What bounds it is Philox (about 55 vector cycles
+// an element) on a batch, 29 us for 64 requests over 151936 logits, and a chain of dependent loads
+// for one request, 13 us. Requests are shared out so that there are about 512 workgroups: 256, 768
+// and 1024 measure 31.6, 29.7 and 29.7 us, since every share merges the slices again.
 template <int TD, int DD>
 __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a) {
   __shared__ RowPart tp[kMaxDrafts + 1], dp[kMaxDrafts];
@@ -453,7 +459,10 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
 // A capture slot lists a position's support: its ids, their logprobs (normalised over the
 // support) and their number. One workgroup per request: its waves look the drafts up in the
 // lists, all positions at once; at the position where the request stops, the drafter's list goes
-// into a hash table in LDS that the target's entries look themselves up in, and race.
+// into a hash table in LDS that the target's entries look themselves up in, and race. A few
+// megabytes move; the time is that of the chain of lookup, decision, table and race: 9 us for
+// supports of 64, 15 us for 256 requests of 4 drafts with supports of up to 2048, and for 64 of 2
+// with up to 8192.
 struct SupportArgs {
   const int32_t* ids;      // slot i of request n at (n * sn + i * sk) * W
   const float* logprobs;   // likewise

@@ -1,8 +1,9 @@
 """Training over captured supports: bindings of ``include/tsc_train.h``.
 
 ``distill_topk`` is differentiable with respect to the student's logits, and so is
-``replay_logprob``. The backward passes run on the stream that the
-forward ran on, allocate the gradient, and synchronise nothing."""
+``replay_logprob``. The backward passes run on the stream that the forward ran on, allocate the
+gradient, and synchronise nothing. Captured into a HIP graph, a backward pass needs leaves that no
+eager graph still holds: torch's engine would accumulate into those outside the capture."""
 from __future__ import annotations
 
 from typing import NamedTuple, Optional
