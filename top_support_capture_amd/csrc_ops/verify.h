@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
   __shared__ int32_t code[kMaxDrafts + 1];
   __shared__ float xt[kMaxDrafts];
   __shared__ int32_t sh_stop;
+  __shared__ uint32_t sh_bound;
   __shared__ float sh_score[kOpWaves];
   __shared__ RacePart sh_best[kOpWaves];
   __shared__ uint64_t sh_key;
@@ -268,52 +269,75 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
     for (int32_t j = tid; j <= K; j += kOpThreads) out_tok[j] = -1, out_lp[j] = __builtin_nanf("");
     if (tid == 0) a.accepted[n] = 0, a.row_status[n] = (int8_t)status;
   };
+  // What the decisions need is asked for at once, each load a microsecond when there is little else
+  // to do: the states of the slices of the wave's first kRows rows, and thread i's draft i.
+  constexpr int kRows = 4;
+  const RowPart none{-__builtin_inff(), INT32_MAX, 0.0};
+  auto part_of = [&](int32_t r) {  // rows past the counts hold nothing, and are not used
+    r = r < a.rows ? r : a.rows - 1;
+    const RowPart p = a.parts[(n * a.rows + r) * a.slices + ((int32_t)lane < a.slices ? (int32_t)lane : 0)];
+    return (int32_t)lane < a.slices ? p : none;
+  };
+  RowPart v[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) v[j] = part_of((int32_t)w + j * kOpWaves);
+  static_assert(kMaxDrafts <= kOpThreads, "a thread a draft");
+  const bool drafts = (int32_t)tid < K;
+  const int32_t my_draft = drafts ? a.draft_tokens[n * K + tid] : -1;
+  const float my_u = drafts ? a.uniforms[n * K + tid] : -1.0f;
+  const uint64_t seed = a.seeds[n], first_position = a.positions[n];
   if (count < 0 || count > K || !(greedy || temperature_ok(T)) || !temperature_ok(Td)) {
     refuse(TSC_ROW_INVALID_PARAM);
     return;
   }
+  const bool valid = (int32_t)tid < count && my_draft >= 0 && my_draft < a.V && my_u >= 0.0f && my_u < 1.0f;
+  const float my_x = valid && !greedy ? Row<TD>::get(trow + (int64_t)tid * a.t_sk + my_draft) : 0.0f;
+  const float my_y = valid && has_draft ? Row<DD>::get(drow + (int64_t)tid * a.d_sk + my_draft) : 0.0f;
+  if (tid == 0) sh_stop = count, sh_bound = 0u;
   const Scale ct = make_scale(greedy ? 1.0f : T), cd = make_scale(Td);
 
   // Every row's state from its slices': a wave a row, a lane a slice.
-  const RowPart none{-__builtin_inff(), INT32_MAX, 0.0};
-  for (int32_t r = (int32_t)w; r < a.rows; r += kOpWaves) {
-    const bool is_draft = r > K;
-    const int32_t i = is_draft ? r - K - 1 : r;
-    if (i > count - (is_draft ? 1 : 0) || (is_draft && !has_draft)) continue;  // wave-uniform
-    const RowPart v = (int32_t)lane < a.slices ? a.parts[(n * a.rows + r) * a.slices + lane] : none;
-    RowPart p = merge_slices(v, is_draft ? cd : ct);
-    if (greedy && p.s == p.s) p.s = 1.0;
-    if (lane == 0) (is_draft ? dp[i] : tp[i]) = p;
+  for (int32_t r0 = (int32_t)w; r0 < a.rows; r0 += kRows * kOpWaves) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int32_t r = r0 + j * kOpWaves;
+      const bool is_draft = r > K;
+      const int32_t i = is_draft ? r - K - 1 : r;
+      // wave-uniform
+      if (r < a.rows && i <= count - (is_draft ? 1 : 0) && !(is_draft && !has_draft)) {
+        RowPart p = merge_slices(v[j], is_draft ? cd : ct);
+        if (greedy && p.s == p.s) p.s = 1.0;
+        if (lane == 0) (is_draft ? dp[i] : tp[i]) = p;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) v[j] = part_of(r0 + (kRows + j) * kOpWaves);
   }
   lds_barrier();
-  for (int32_t i = (int32_t)tid; i <= count; i += kOpThreads) {
+  for (int32_t i = (int32_t)tid; i <= count; i += kOpThreads) {  // the second time round past the drafts
     const RowPart t = tp[i];
     int32_t st = part_status(t), c = kBonus;
     if (i < count) {
-      const int32_t d = a.draft_tokens[n * K + i];
-      const float u = a.uniforms[n * K + i];
-      const bool valid = d >= 0 && d < a.V && u >= 0.0f && u < 1.0f;
       if (has_draft && st == TSC_ROW_OK) st = part_status(dp[i]);
       if (!valid) st = TSC_ROW_INVALID_PARAM;
       if (st == TSC_ROW_OK) {
         if (greedy) {
-          c = d == t.at ? kAccepted : kRejected;
+          c = my_draft == t.at ? kAccepted : kRejected;
           xt[i] = t.m;
         } else {
-          xt[i] = Row<TD>::get(trow + i * a.t_sk + d);
-          const double p = exp(((double)xt[i] - (double)t.m) / (double)T) / t.s;
+          xt[i] = my_x;
+          const double p = exp(((double)my_x - (double)t.m) / (double)T) / t.s;
           double q = 1.0;
-          if (has_draft) {
-            const float xd = Row<DD>::get(drow + i * a.d_sk + d);
-            q = exp(((double)xd - (double)dp[i].m) / (double)Td) / dp[i].s;
-          }
-          c = (double)u * q < p ? kAccepted : kRejected;
+          if (has_draft) q = exp(((double)my_y - (double)dp[i].m) / (double)Td) / dp[i].s;
+          c = (double)my_u * q < p ? kAccepted : kRejected;
         }
       }
     }
     code[i] = st == TSC_ROW_OK ? c : kStatus + st;
+    if (code[i] != kAccepted) atomicMin(&sh_stop, i);
   }
-  const Decision dec = first_stop(code, count, &sh_stop);
+  lds_barrier();
+  const Decision dec{sh_stop, code[sh_stop]};
   if (dec.code >= kStatus) {
     refuse(dec.code - kStatus);
     return;
@@ -347,7 +371,7 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
   const RowPart d = subtract ? dp[stop] : RowPart{0.0f, 0, 1.0};
   const TB* tr = trow + (int64_t)stop * a.t_sk;
   const DB* dr = drow + (int64_t)stop * a.d_sk;
-  const uint64_t seed = a.seeds[n], position = a.positions[n] + (uint64_t)stop;
+  const uint64_t position = first_position + (uint64_t)stop;
   const int64_t lo = share * a.share_len, hi = lo + a.share_len < a.V ? lo + a.share_len : a.V;
   auto exact = [&](float xe, float ye) -> double {
     double p = exp(((double)xe - (double)t.m) / (double)T) / t.s;
@@ -357,7 +381,7 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
   const float c_t = plain_scale(T), c_d = plain_scale(Td);
   const float lg_t = -__builtin_amdgcn_logf((float)t.s), lg_d = -__builtin_amdgcn_logf((float)d.s);
   RaceEntry best;
-  float bound = 0.0f;  // the wave's best score so far, less the margin
+  float bound = 0.0f;  // the workgroup's best score so far, as far as this wave knows, less the margin
   const uint32_t stream = rejected ? 1u : 0u;
   constexpr int64_t kStep = (int64_t)kOpThreads * 8;
   const int64_t first = lo + (int64_t)tid * 8;
@@ -378,29 +402,31 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
     float tt[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) tt[e] = race_t(word[e >> 2][e & 3]);
-    // Few lanes have an entry that can still win; those are computed again, one by one. The first
-    // draws make a bound from each lane's heaviest entry, before all of its entries are open.
-#pragma unroll 1
-    for (int turn = bound == 0.0f ? 0 : 1; turn < 2; ++turn) {
-      uint32_t open = 0;
-      if (turn == 0) {
-        float w = 0.0f;
+    bound = __builtin_fmaxf(bound, __uint_as_float(__hip_atomic_load(&sh_bound, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)));
+    if (bound == 0.0f) {  // the first chunk makes its own
+      float sc = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (w8[e] > w) w = w8[e], open = 1u << e;
-      } else {
+      for (int e = 0; e < 8; ++e)
+        if (!RaceEntry::race_near(p[e], w8[e]))
+          sc = __builtin_fmaxf(sc, w8[e] * __builtin_amdgcn_rcpf(race_exponential(tt[e])));
+      bound = wave_max(sc) * (1.0f - kRaceClose);
+    }
+    // Few lanes have an entry that can still win; those are computed again, one by one.
+    uint32_t open = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) open |= RaceEntry::can_win(p[e], w8[e], tt[e], bound) ? 1u << e : 0u;
-      }
-      if (__ballot(open != 0u) == 0) continue;
-      while (open != 0u) {
-        const int64_t id = at + __builtin_ctz(open);
-        open &= open - 1u;
-        const float xe = Row<TD>::get(tr + id), ye = subtract ? Row<DD>::get(dr + id) : 0.0f;
-        best.offer(weight_of(xe, t.m, c_t, lg_t), subtract ? weight_of(ye, d.m, c_d, lg_d) : 0.0f,
-                   (int32_t)id, race_t(race_word((uint32_t)id, stream, seed, position)), xe, ye, exact);
-      }
-      bound = __builtin_fmaxf(bound, wave_max(best.score) * (1.0f - kRaceClose));
+    for (int e = 0; e < 8; ++e) open |= RaceEntry::can_win(p[e], w8[e], tt[e], bound) ? 1u << e : 0u;
+    if (__ballot(open != 0u) == 0) return;
+    while (open != 0u) {
+      const int64_t id = at + __builtin_ctz(open);
+      open &= open - 1u;
+      const float xe = Row<TD>::get(tr + id), ye = subtract ? Row<DD>::get(dr + id) : 0.0f;
+      best.offer(weight_of(xe, t.m, c_t, lg_t), subtract ? weight_of(ye, d.m, c_d, lg_d) : 0.0f,
+                 (int32_t)id, race_t(race_word((uint32_t)id, stream, seed, position)), xe, ye, exact);
+    }
+    const float top = wave_max(best.score) * (1.0f - kRaceClose);
+    if (top > bound || bound == 0.0f) {
+      bound = __builtin_fmaxf(bound, top);
+      if (lane == 0) atomicMax(&sh_bound, __float_as_uint(bound));
     }
   };
   // Whole chunks are asked for kAhead steps before their turn: with few waves to a CU, that many
