@@ -209,7 +209,7 @@ __device__ inline RacePart race_winner(const RaceEntry& e, Weight weight, float*
   return b;
 }
 
-// Where a request stops, and why: filled in by decide().
+// Where a request stops, and why.
 struct Decision {
   int32_t stop;    // index of the first draft that is not accepted; the count when all are
   int32_t code;    // kRejected, kBonus, or kStatus + a row status
@@ -234,10 +234,10 @@ __device__ inline Decision first_stop(const int32_t* code, int32_t count, int32_
   return {stop, code[stop]};
 }
 
-// The race at the position where a request stops. What bounds it is Philox (about 55 vector cycles
-// an element) on a batch, 29 us for 64 requests over 151936 logits, and a chain of dependent loads
-// for one request, 13 us. Requests are shared out so that there are about 512 workgroups: 256, 768
-// and 1024 measure 31.6, 29.7 and 29.7 us, since every share merges the slices again.
+// The race at the position where a request stops. On a batch it is bound by Philox and the weights,
+// about 1300 cycles of a SIMD for 512 elements: 27 us for 64 requests over 151936 logits; for one
+// request by a chain of dependent steps, 12 us. Requests are shared out so that there are about 512
+// workgroups (384, 640, 768 and 1024: 30.6, 29.9, 27.8 and 27.8 us against 28.0).
 template <int TD, int DD>
 __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a) {
   __shared__ RowPart tp[kMaxDrafts + 1], dp[kMaxDrafts];
@@ -429,9 +429,10 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
       if (lane == 0) atomicMax(&sh_bound, __float_as_uint(bound));
     }
   };
-  // Whole chunks are asked for kAhead steps before their turn: with few waves to a CU, that many
-  // bytes on the way are what keeps the memory busy.
-  constexpr int kAhead = 3;
+  // Whole chunks are asked for kAhead steps before their turn, since there are few waves to a CU
+  // (bfloat16 27 us for 1, 2 or 3 steps; float32, 64 requests over 151936, 25.8, 24.6 and 28.3: three
+  // steps of both rows no longer fit the registers).
+  constexpr int kAhead = 2;
   typename Row<TD>::Chunk vx[kAhead];
   typename Row<DD>::Chunk vy[kAhead] = {};
   const int64_t most_at = hi >= lo + 8 ? hi - 8 : -1;  // the last place of a whole chunk
