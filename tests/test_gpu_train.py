@@ -506,6 +506,31 @@ def test_whole_backward_pass_in_a_graph():
         assert torch.equal(step(c["xt"]), want)
 
 
+def test_offsets_past_32_bits():
+    # Rows whose elements lie more than 2^31 elements into logits and gradient; all but the last two
+    # are padding (length 0), which is not read and has gradient 0.
+    log("case gradients of 70000 rows of 32000")
+    rng = np.random.default_rng(37)
+    N, V, W = 70000, 32000, 16
+    c = replay_case(rng, 2, V, W, "bf16")
+    x = torch.empty(N, V, dtype=torch.bfloat16, device=DEV)
+    x[-2:] = c["xt"]
+    put = lambda a, dt: torch.cat([torch.zeros((N - 2, *a.shape[1:]), dtype=dt, device=DEV), tensor(a, dt)])
+    ids, lengths = put(c["ids"], torch.int32), put(c["lengths"], torch.int32)
+    tok, T = put(c["tok"], torch.int32), put(c["T"], torch.float32)
+    weights, values = rng.standard_normal(2).astype(np.float32), rng.standard_normal((2, W)).astype(np.float32)
+    w = put(weights, torch.float32)
+    one = tsc.distill_topk_grad(x, ids, put(values, torch.float32), lengths, T + (T == 0), w)
+    check_distill(c["x"], "bf16", c["T"], c["ids"], values, c["lengths"], None, weights, one.loss[-2:],
+                  one.row_status[-2:], one.grad_logits[-2:])
+    assert torch.all(one.row_status[:-2] == 2) and all(torch.all(one.grad_logits[n : n + 5000] == 0)
+                                                       for n in range(0, N - 5000, 5000))
+    del one
+    grad = tsc.replay_logprob_backward(x, T, ids, lengths, tok, w)
+    check_replay_grad(c, "bf16", weights, None, grad[-2:])
+    assert all(torch.all(grad[n : n + 5000] == 0) for n in range(0, N - 5000, 5000))
+
+
 def test_empty_batches():
     log("case training calls without rows")
     z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device=DEV)

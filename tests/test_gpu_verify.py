@@ -322,6 +322,21 @@ def test_in_a_graph_and_on_another_stream():
         assert torch.equal(o.tokens, want[k].tokens) and torch.equal(o.accepted, want[k].accepted)
 
 
+def test_offsets_past_32_bits():
+    log("case verify with requests 2^31 + 24 elements apart")
+    rng = np.random.default_rng(41)
+    N, K, V = 2, 2, 1001
+    c = case(rng, N, K, V, "bf16")
+    buf = torch.empty(2**31 + 24 + (K + 1) * V, dtype=torch.bfloat16, device=DEV)
+    t = buf.as_strided((N, K + 1, V), (2**31 + 24, V, 1))
+    t.copy_(c["t"])
+    T = np.ones(N, np.float32)
+    assert check_verified(run(dict(c, t=t), T), ref(c, T), V) == 0
+    d = buf.as_strided((N, K, V), (2**31 + 24, V, 1))
+    d.copy_(c["d"])
+    assert check_verified(run(dict(c, d=d), T), ref(c, T), V) == 0
+
+
 def test_empty_batch():
     log("case verify without requests")
     z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device=DEV)
