@@ -372,6 +372,19 @@ def test_replay_gradient_of_long_supports(V, W, dtype, both):
     assert np.all(off <= ok), (np.argmax(off - ok), off.max(), ok[np.argmax(off - ok)])
 
 
+@pytest.mark.parametrize("V,W,dtype", [(70001, 6000, "bf16"), (40003, 2500, "f32"), (140000, 64, "bf16")])
+def test_replay_gradient_of_many_wide_rows(V, W, dtype):
+    # Rows enough that each is one workgroup's, bitmask rows and long packed rows among short ones.
+    log(f"case replay gradient of many wide rows V={V} W={W} {dtype}")
+    rng = np.random.default_rng(V)
+    N = 131
+    c = replay_case(rng, N, V, W, dtype, wide=0.5, pad=3, base=1)
+    args, kw = replay_inputs(c, True)
+    gs = rng.standard_normal(N).astype(np.float32)
+    grad = tsc.replay_logprob_backward(c["xt"], *args, tensor(gs, torch.float32), **kw)
+    check_replay_grad(c, dtype, gs, None, grad)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_replay_gradient_edges(dtype):
     log(f"case replay gradient edges {dtype}")

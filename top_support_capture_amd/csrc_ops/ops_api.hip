@@ -212,7 +212,7 @@ template <int DT>
 hipError_t launch_replay_grad(const tsc::ReplayGradArgs& a, bool streams, hipStream_t s) {
   static std::atomic<uint64_t> with{0}, without{0};
   const int64_t groups = a.N * a.segments;
-  return streams ? launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<DT, true>, a, groups, with, s, 0, a.mask_bytes)
+  return streams ? launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<DT, true>, a, groups, with, s, (size_t)a.lds_bytes, a.mask_bytes)
                  : launch_grad<tsc::kGradThreads>(&tsc::replay_grad_kernel<DT, false>, a, groups, without, s);
 }
 
@@ -397,9 +397,15 @@ int32_t tsc_replay_logprob_backward(const void* logits, int32_t dtype, int64_t N
     return TSC_ERR_INVALID_ARGUMENT;
   const Cut cut = grad_cut(N, V, 256);
   const Dense dense = dense_rows(V, W);
+  using Ent = tsc::Entries<tsc::kGradThreads>;
+  // A streamed row that its workgroup writes whole is kept in LDS as far as it goes, for the second
+  // pass (bf16: 256 rows of 129280 37.1 -> 34.8 us, 512 of 151936 92 -> 85; short rows come from the
+  // L2 as fast, and all of a CU's LDS costs each workgroup 0.7 us: 1024 rows of 32000 52 against 50).
+  const bool hold = cut.n == 1 && V * (dtype == TSC_DTYPE_F32 ? 4 : 2) > 128 * 1024;
   const tsc::ReplayGradArgs a{logits, N, V, ld, temperature, packed_ids, lengths, W, capture_status,
                               support_bits, bits_ld, tokens, grad_selected, grad_logprobs,
-                              grad_logits, cut.n, cut.len, dense.above, dense.mask_bytes};
+                              grad_logits, cut.n, cut.len, dense.above, dense.mask_bytes,
+                              (int32_t)(hold ? (size_t)Ent::kAll : Ent::bytes(W, dense.mask_bytes)), hold};
   (void)hipGetLastError();
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool streams = support_bits != nullptr || dense.mask_bytes > 0;

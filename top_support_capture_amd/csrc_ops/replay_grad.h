@@ -8,8 +8,10 @@
 //
 // Measured for bfloat16: 256 rows of 151936 with supports of up to 2048 take 23 us, 78 MB written
 // and 27 MB of gathered lines; 256 rows of 129280, three in four of them bitmask rows of about 10000
-// members, 37 us (195 MB: two readings and a write). 1024 rows of 151936 with 2048 entries 110 us.
+// members, 35 us (195 MB: two readings and a write). 1024 rows of 151936 with 2048 entries 110 us.
 #pragma once
+
+#include <type_traits>
 
 #include "row_stats.h"
 
@@ -33,6 +35,8 @@ struct ReplayGradArgs {
   int64_t seg_len;
   int32_t dense;       // packed rows longer than this are streamed under a bitmask in LDS
   int32_t mask_bytes;  // of that bitmask, for V bits; 0 where no row is that long
+  int32_t lds_bytes;   // of dynamic LDS, where rows are streamed
+  int32_t hold;        // whether streamed rows are kept in it as far as it goes
 };
 
 constexpr int kGradThreads = 1024;
@@ -73,15 +77,44 @@ struct PackedEntries {
   }
 };
 
+// The first chunks of a streamed row, kept in LDS from the first pass over it to the second where
+// no entries need the room: `steps` of a chunk a thread.
+template <int DT>
+struct HeldChunks {
+  using Chunk = typename Row<DT>::Chunk;
+  static constexpr int kParts = sizeof(Chunk) / 16;
+  u32x4* at;
+  int32_t steps;
+  __device__ inline HeldChunks(void* lds, int32_t bytes)
+      : at(reinterpret_cast<u32x4*>(lds)), steps(bytes / (int32_t)(kGradThreads * sizeof(Chunk))) {}
+  __device__ inline void put(int64_t step, const Chunk& c) const {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      at[(step * kParts + i) * kGradThreads + threadIdx.x] = reinterpret_cast<const u32x4*>(&c)[i];
+  }
+  __device__ inline Chunk get(int64_t step) const {
+    Chunk c;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      reinterpret_cast<u32x4*>(&c)[i] = at[(step * kParts + i) * kGradThreads + threadIdx.x];
+    return c;
+  }
+};
+
+struct NoneHeld {
+  static constexpr int32_t steps = 0;
+};
+
 // Mask bytes and logits of a bitmask row, kAhead windows before their turn. Lanes past the last
 // whole chunk of [lo, hi) ask for the first one, and use nothing of it.
-template <int DT, class Mask>
+template <int DT, class Mask, class Held>
 struct MaskedStream {
   static constexpr int kSize = Window<kGradThreads>::kSize;
   static constexpr int kAhead = DT == TSC_DTYPE_BF16 ? 4 : 2;
   const typename Row<DT>::Bits* row;
   Mask bits;
   int64_t lo, hi;
+  Held held;
   typename Row<DT>::Chunk v[kAhead];
   uint32_t b[kAhead];
   __device__ inline int64_t place(int k) const { return lo + (int64_t)k * kSize + (int64_t)threadIdx.x * 8; }
@@ -89,6 +122,12 @@ struct MaskedStream {
     if (lo + 8 > hi) return;
     const int64_t at = place(k) + 8 <= hi ? place(k) : lo;
     b[j] = bits[at >> 3];
+    if constexpr (!std::is_same<Held, NoneHeld>::value) {
+      if (k < held.steps) {  // uniform
+        v[j] = held.get(k);
+        return;
+      }
+    }
     v[j] = Row<DT>::load(row + at);
   }
   // use(k, at, x, mask) for every window k of the segment, the logits of non-members as they are.
@@ -154,8 +193,7 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
   uint32_t flags = 0;  // 1: an id out of range, 2: an element of the support, 4: the token is one
   // A long packed row is turned into a bitmask in LDS and treated as a bitmask row, unless an id
   // occurs twice.
-  uint32_t* own = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(dyn_lds) +
-                                              Entries<kGradThreads>::bytes(a.W, a.mask_bytes) - a.mask_bytes);
+  uint32_t* own = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(dyn_lds) + (a.lds_bytes - a.mask_bytes));
   bool streamed = kStreams && from_bits;
   if (kStreams && !from_bits && len > a.dense) {
     for (int32_t i = tid; i < a.mask_bytes / 4; i += kGradThreads) own[i] = 0u;
@@ -195,8 +233,9 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
   double G = 0.0;
   if (entries) first.load(ids, gl, row, streamed, a.V, len, tid);
   if (longer) second.load(ids, gl, row, streamed, a.V, len, tid + kFirst * kGradThreads);
-  ent.begin();
+  if (entries) ent.begin();
   lds_barrier();
+  HeldChunks<DT> held(dyn_lds, streamed && !entries && a.hold ? a.lds_bytes - a.mask_bytes : 0);
   auto look = [&](auto& t, int32_t i0) {
     if (!streamed) st.add(t.x, c);
 #pragma unroll
@@ -245,6 +284,7 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
           f[u * 8 + e] = __uint_as_float((__float_as_uint(f[u * 8 + e]) & keep) | (0xFF800000u & ~keep));
         }
         any |= b[u];
+        if (base / kStep + u < held.steps) held.put(base / kStep + u, v[u]);
         ask(u, base + start + (kU + u) * kStep);
       }
       st.add(f, c);
@@ -280,7 +320,7 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
   const double ws = wave_reduce(rescaled(st.s, st.m, m, c), SumOp());
   G = wave_reduce(G, SumOp());
   if (lane == 0) sh.s[w] = ws, sh.g[w] = G;
-  ent.offsets();
+  if (entries) ent.offsets();
   lds_barrier();
   double S = sh.s[0];
   G = sh.g[0];
@@ -344,9 +384,8 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
     store8<DT>(out, at, hi, r);
   };
   auto write_row = [&](auto mask) {
-    MaskedStream<DT, decltype(mask)> stream{row, mask, lo, hi};
     if (entries) {
-      stream.run([&](int k, int64_t at, float (&v)[8], uint32_t b) {
+      MaskedStream<DT, decltype(mask), NoneHeld>{row, mask, lo, hi, {}}.run([&](int k, int64_t at, float (&v)[8], uint32_t b) {
         ent.turn(k, add, [&] {
           if (at >= hi) return;
           float r[8];
@@ -355,7 +394,7 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
         });
       });
     } else {  // the token alone has an upstream gradient: no windows, no barriers
-      stream.run([&](int, int64_t at, float (&v)[8], uint32_t b) {
+      MaskedStream<DT, decltype(mask), HeldChunks<DT>>{row, mask, lo, hi, held}.run([&](int, int64_t at, float (&v)[8], uint32_t b) {
         if (at >= hi) return;
         float r[8] = {};
         if (at >> 3 == tok >> 3) {
