@@ -82,7 +82,8 @@ size_t tsc_distill_topk_grad_workspace(int64_t N, int64_t V);
  * the support logprob of packed id i plus, at the row's token, that of the selected logprob:
  *     grad_logits[n, j] = (G_j - pi_j sum_{i in S} G_i) / T   for j in S, 0 elsewhere.
  *
- * logits .. tokens  as given to tsc_replay_logprob. The packed ids of a row are distinct.
+ * logits .. tokens  as given to tsc_replay_logprob. The packed ids of a row are distinct (one that
+ *              occurs twice counts twice, as it does there).
  * grad_selected [N] float32 or NULL (0): upstream gradient of selected_logprob. It has no effect
  *              on a row whose token is not in its support (whose logprob is -inf).
  * grad_logprobs [N, W] float32 or NULL (0): upstream gradient of logprobs; entries past lengths[n]

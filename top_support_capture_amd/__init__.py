@@ -300,8 +300,9 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
     where ``capture_status`` (int8 [N]) is OVERFLOW, the row of ``support_bits`` (uint8 [N, ld]).
     ``temperature`` float32 [N] divides the logits first (1 = the plain masked log-softmax).
 
-    Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``);
-    with ``stream`` given, their backward pass runs there too."""
+    Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``)
+    and to nothing else: ``temperature`` is taken as a constant. With ``stream`` given, their backward
+    pass runs there too."""
     others = (temperature, packed_ids, lengths, tokens, capture_status, support_bits)
     out = _replay_forward(logits, *others, return_logprobs, stream)
     if logits.requires_grad and torch.is_grad_enabled():
