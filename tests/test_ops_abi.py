@@ -167,6 +167,13 @@ def test_binding_refuses_bad_tensors():
             tsc.replay_logprob_backward(bad, z(2), z(2, 4, dt=i), z(2, dt=i), z(2, dt=i), z(2))
 
 
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+    from top_support_capture_amd import _launch
+    with pytest.raises(ValueError):
+        _launch(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)), lambda s: s)
+
+
 def test_capture_layouts_are_checked():
     from top_support_capture_amd.verify import Support, _slots
     cpu = torch.device("cpu")

@@ -152,6 +152,8 @@ def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], go):
     launch and the allocations around it; the usual case costs no context switch."""
     if stream is None and dev.index == torch.cuda.current_device():
         return go(torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream must be on {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         return go(torch.cuda.current_stream(dev).cuda_stream)
 

@@ -28,7 +28,6 @@ struct Row<TSC_DTYPE_BF16> {
   using Bits = uint16_t;
   struct Chunk {
     u32x4 v;
-    __device__ inline void hide() { asm volatile("" : "+v"(v)); }  // a value the compiler cannot see through
   };
   __device__ static inline Chunk load(const Bits* p) {
     return {*reinterpret_cast<const u32x4_by2*>(p)};
@@ -64,7 +63,6 @@ struct Row<TSC_DTYPE_F32> {
   using Bits = float;
   struct Chunk {
     u32x4 v[2];
-    __device__ inline void hide() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
   };
   __device__ static inline Chunk load(const Bits* p) {
     const u32x4_by4* q = reinterpret_cast<const u32x4_by4*>(p);
@@ -114,11 +112,6 @@ __device__ inline void store8(typename Row<DT>::Bits* row, int64_t at, int64_t e
     for (int e = 0; e < 8; ++e)
       if (at + e < end) Row<DT>::put(row + at + e, x[e]);
   }
-}
-
-__device__ inline float get_any(const void* row, int64_t at, int dtype) {
-  return dtype == TSC_DTYPE_F32 ? Row<TSC_DTYPE_F32>::get((const float*)row + at)
-                                : Row<TSC_DTYPE_BF16>::get((const uint16_t*)row + at);
 }
 
 // A temperature the sampler takes for sampling: normal, positive, finite.
