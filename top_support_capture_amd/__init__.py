@@ -314,10 +314,6 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
 
 def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_status, support_bits,
                     return_logprobs, stream=None) -> ReplayOutput:
-    if stream is None and logits.is_cuda and logits.device.index != torch.cuda.current_device():
-        with torch.cuda.device(logits.device):
-            return _replay_forward(logits, temperature, packed_ids, lengths, tokens,
-                                   capture_status, support_bits, return_logprobs)
     lib = library()
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [N, V] with unit column stride")
@@ -325,6 +321,8 @@ def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_st
         raise ValueError("logits must be float32 or bfloat16")
     dt = TSC_DTYPE_BF16 if logits.dtype == torch.bfloat16 else TSC_DTYPE_F32
     dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("logits must be on a GPU")
     N, V = logits.shape
     ld = logits.stride(0) if N > 1 else V
     _check(temperature, "temperature", torch.float32, N, dev)
@@ -343,19 +341,19 @@ def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_st
                 or not support_bits.is_contiguous()):
             raise ValueError(f"support_bits must be a contiguous uint8 tensor [{N}, ld] on {dev}")
         bits_ld = int(support_bits.shape[1])
-    out = ReplayOutput(torch.empty(N, dtype=torch.float32, device=dev),
-                       torch.empty((N, W), dtype=torch.float32, device=dev)
-                       if return_logprobs else None,
-                       torch.empty(N, dtype=torch.int8, device=dev))
-    if stream is None and dev.type == "cuda":
-        s = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        s = (stream or torch.cuda.current_stream(dev)).cuda_stream
-    code = lib.tsc_replay_logprob(logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(),
-                                  packed_ids.data_ptr(), lengths.data_ptr(), W,
-                                  _ptr(capture_status), _ptr(support_bits), bits_ld,
-                                  tokens.data_ptr(), out.selected_logprob.data_ptr(),
-                                  _ptr(out.logprobs), out.row_status.data_ptr(), s)
+
+    def go(s):
+        out = ReplayOutput(torch.empty(N, dtype=torch.float32, device=dev),
+                           torch.empty((N, W), dtype=torch.float32, device=dev)
+                           if return_logprobs else None,
+                           torch.empty(N, dtype=torch.int8, device=dev))
+        return out, lib.tsc_replay_logprob(logits.data_ptr(), dt, N, V, ld, temperature.data_ptr(),
+                                           packed_ids.data_ptr(), lengths.data_ptr(), W,
+                                           _ptr(capture_status), _ptr(support_bits), bits_ld,
+                                           tokens.data_ptr(), out.selected_logprob.data_ptr(),
+                                           _ptr(out.logprobs), out.row_status.data_ptr(), s)
+
+    out, code = _launch(dev, stream, go)
     if code != 0:
         raise TscError(code, lib.tsc_status_string(code).decode())
     return out
