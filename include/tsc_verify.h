@@ -95,10 +95,11 @@ size_t tsc_verify_drafts_workspace(int64_t N, int32_t K, int64_t V, int32_t has_
  *              draft). Ids within a slot are distinct.
  * The other arguments are those of tsc_verify_drafts (uniforms are read for every draft); a draft
  * that the target's support does not hold is never accepted. logprobs are the capture's.
- * row_status   TSC_ROW_OK; TSC_ROW_INVALID_PARAM (count, a length outside [1, W], a negative draft,
- *              a uniform out of range); the slot's own status when that is not TSC_ROW_OK
- *              (a support wider than W is not whole: TSC_ROW_OVERFLOW); TSC_ROW_NONFINITE when no
- *              logprob of the last slot is a number. Only positions that are reached count.
+ * row_status   TSC_ROW_OK; TSC_ROW_INVALID_PARAM (count, a length outside [1, W], a slot status that
+ *              is no TSC_ROW_* code, a negative draft, a uniform out of range); the slot's own
+ *              status when that is not TSC_ROW_OK (a support wider than W is not whole:
+ *              TSC_ROW_OVERFLOW); TSC_ROW_NONFINITE when no logprob of the last slot is a number.
+ *              Only positions that are reached count.
  * Needs no workspace.
  */
 int32_t tsc_verify_captured(const int32_t* target_ids, const float* target_logprobs,

@@ -28,6 +28,8 @@ import numpy as np
 from .philox import philox4
 from .sampler import (FLT_MIN, ROW_INVALID_PARAM, ROW_NO_SUPPORT, ROW_NONFINITE, ROW_OK)
 
+ROW_ABORTED = 5  # a sampler row that gave up waiting, which has no oracle: the last status there is
+
 
 @dataclasses.dataclass
 class Request:
@@ -155,7 +157,7 @@ def verify_drafts(target, tokens, T, uniforms, seeds, positions, draft=None, cou
 def slot_position(ids, logprobs, length, status) -> Position:
     W = ids.size
     if status != ROW_OK:
-        return int(status), ids, logprobs
+        return int(status) if ROW_OK < status <= ROW_ABORTED else ROW_INVALID_PARAM, ids, logprobs
     if not 1 <= length <= W:
         return ROW_INVALID_PARAM, ids, logprobs
     order = np.argsort(ids[:length], kind="stable")

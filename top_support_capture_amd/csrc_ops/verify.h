@@ -517,10 +517,11 @@ struct CapturedArgs {
 constexpr int kCapThreads = 1024;
 constexpr int kCapWaves = kCapThreads / kWaveSize;
 
-// The slot's status: a capture that is not whole cannot be verified against.
+// The slot's status: a capture that is not whole cannot be verified against. A number that is no row
+// status is INVALID_PARAM: the codes of decisions are told from statuses by their range.
 __device__ inline int32_t slot_status(const SupportArgs& s, int64_t slot) {
   const int32_t st = s.status ? (int32_t)s.status[slot] : TSC_ROW_OK;
-  if (st != TSC_ROW_OK) return st;
+  if (st != TSC_ROW_OK) return st > TSC_ROW_OK && st <= TSC_ROW_ABORTED ? st : TSC_ROW_INVALID_PARAM;
   const int32_t n = s.lengths[slot];
   return n >= 1 && n <= s.W ? TSC_ROW_OK : TSC_ROW_INVALID_PARAM;
 }
