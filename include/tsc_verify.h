@@ -54,13 +54,13 @@ extern "C" {
  * draft_tokens [N, K] int32, in [0, V).
  * draft_counts [N] int32 in [0, K], or NULL (K each): how many drafts a request has. Rows past
  *              them are not read.
- * uniforms     [N, K] float32 in [0, 1).
+ * uniforms     [N, K] float32 in [0, 1); those of greedy requests may hold anything.
  * seeds, positions [N] uint64.
  * tokens       [N, K + 1] int32 out: the accepted drafts, then the drawn token, then -1.
  * accepted     [N] int32 out: number of accepted drafts.
  * logprobs     [N, K + 1] float32 out: log p of each emitted token, NaN after them.
- * row_status   [N] int8 out: TSC_ROW_OK; TSC_ROW_INVALID_PARAM (temperature, count, or a draft or
- *              uniform out of range); TSC_ROW_NONFINITE (a row with a NaN or +inf) or
+ * row_status   [N] int8 out: TSC_ROW_OK; TSC_ROW_INVALID_PARAM (temperature, count, or a draft or,
+ *              unless greedy, uniform out of range); TSC_ROW_NONFINITE (a row with a NaN or +inf) or
  *              TSC_ROW_NO_SUPPORT (a row that is -inf throughout). Only positions that the
  *              verification reaches count, in their order. Unless OK, the request's tokens are
  *              -1, its accepted 0 and its logprobs NaN.

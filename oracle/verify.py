@@ -69,7 +69,8 @@ def _value(pos: Position, token: int) -> float:
 
 def verify_request(K: int, count: int, drafts, uniforms, seed: int, position: int,
                    target: Callable[[int], Position], draft: Optional[Callable[[int], Position]],
-                   ok_token: Callable[[int], bool], params_ok: bool = True) -> Request:
+                   ok_token: Callable[[int], bool], params_ok: bool = True,
+                   greedy: bool = False) -> Request:
     tokens, lps = np.full(K + 1, -1, np.int32), np.full(K + 1, np.nan)
 
     def refused(status):
@@ -81,6 +82,8 @@ def verify_request(K: int, count: int, drafts, uniforms, seed: int, position: in
     for i in range(count + 1):
         if i < count:
             d, u = int(drafts[i]), float(np.float32(uniforms[i]))
+            if greedy:
+                u = 0.0  # p is 1 or 0: the uniform plays no part
             if not ok_token(d) or not 0.0 <= u < 1.0:
                 return refused(ROW_INVALID_PARAM)
         p = target(i)
@@ -150,7 +153,7 @@ def verify_drafts(target, tokens, T, uniforms, seeds, positions, draft=None, cou
             K, K if counts is None else int(counts[n]), tokens[n], uniforms[n], int(seeds[n]),
             int(positions[n]), position,
             (lambda i, n=n, td=td: softmax_position(draft[n, i], td)) if use else None,
-            lambda d: 0 <= d < V, ok))
+            lambda d: 0 <= d < V, ok, greedy))
     return out
 
 

@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
     refuse(TSC_ROW_INVALID_PARAM);
     return;
   }
-  const bool valid = (int32_t)tid < count && my_draft >= 0 && my_draft < a.V && my_u >= 0.0f && my_u < 1.0f;
+  const bool valid = (int32_t)tid < count && my_draft >= 0 && my_draft < a.V &&
+                     (greedy || (my_u >= 0.0f && my_u < 1.0f));  // greedy requests use no uniforms
   const float my_x = valid && !greedy ? Row<TD>::get(trow + (int64_t)tid * a.t_sk + my_draft) : 0.0f;
   const float my_y = valid && has_draft ? Row<DD>::get(drow + (int64_t)tid * a.d_sk + my_draft) : 0.0f;
   if (tid == 0) sh_stop = count, sh_bound = 0u;
