@@ -16,6 +16,7 @@ from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
 import torch  # must come first: the library binds to the HIP runtime PyTorch has loaded
+from torch.autograd import forward_ad
 
 __all__ = ["sample_with_mask", "prepare", "PreparedSample", "SampleOutput", "workspace_size",
            "support_bits_ld", "replay_logprob", "ReplayOutput", "support_csr", "SupportCsr",
@@ -162,6 +163,14 @@ def _on(stream: Optional[torch.cuda.Stream]):
     return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _refuse_tangents(call: str, *tensors: Optional[torch.Tensor]) -> None:
+    """The derivatives are reverse-mode ones: the tangent of a dual tensor would be lost in silence."""
+    if forward_ad._current_level < 0:  # outside any dual level, which costs next to nothing to see
+        return
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{call} has no forward-mode derivative")
+
+
 def _check(t: torch.Tensor, name: str, dtype, n: int, dev) -> None:
     if t.device != dev or t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape [{n}] on {dev}")
@@ -304,7 +313,8 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
 
     Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``)
     and to nothing else: ``temperature`` is taken as a constant. With ``stream`` given, their backward
-    pass runs there too."""
+    pass runs there too. There is no forward-mode derivative: dual tensors are refused."""
+    _refuse_tangents("replay_logprob", logits, temperature)
     others = (temperature, packed_ids, lengths, tokens, capture_status, support_bits)
     out = _replay_forward(logits, *others, return_logprobs, stream)
     if logits.requires_grad and torch.is_grad_enabled():
