@@ -1,5 +1,6 @@
 """What the Python binding of the operators around captures refuses before any launch (no GPU needed:
 tensors without storage stand in for GPU tensors)."""
+import warnings
 from types import SimpleNamespace
 
 import pytest
@@ -77,3 +78,20 @@ def test_tangents_of_upstream_gradients_are_refused(which, monkeypatch):
             out = tsc.replay_logprob(leaf, one, ids, lengths, tok).selected_logprob
         with pytest.raises(NotImplementedError, match="forward-mode"):
             (out * weights).sum().backward()
+
+
+# ---- gradients that do not exist --------------------------------------------------------------------
+
+def test_replay_says_that_no_gradient_reaches_the_temperature(monkeypatch):
+    one, i = torch.ones(2), dict(dtype=torch.int32)
+    monkeypatch.setattr(tsc, "_replay_forward", lambda *a: tsc.ReplayOutput(one.clone(), None, one.char()))
+    call = lambda x, T: tsc.replay_logprob(x, T, torch.zeros(2, 3, **i), torch.ones(2, **i), torch.zeros(2, **i))
+    leaf, T = torch.zeros(2, 8, requires_grad=True), torch.ones(2, requires_grad=True)
+    with pytest.warns(UserWarning, match="temperature as a constant"):
+        assert call(leaf, T).selected_logprob.requires_grad
+    with warnings.catch_warnings():  # no graph, or no gradient asked for: nothing to say
+        warnings.simplefilter("error")
+        call(leaf, T.detach())
+        call(leaf.detach(), T)
+        with torch.no_grad():
+            call(leaf, T)

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
@@ -312,12 +313,16 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
     ``temperature`` float32 [N] divides the logits first (1 = the plain masked log-softmax).
 
     Both logprob outputs are differentiable with respect to ``logits`` (``replay_logprob_backward``)
-    and to nothing else: ``temperature`` is taken as a constant. With ``stream`` given, their backward
+    and to nothing else: ``temperature`` is taken as a constant (with a warning if it asks for a gradient
+    that would not reach it). With ``stream`` given, their backward
     pass runs there too. There is no forward-mode derivative: dual tensors are refused."""
     _refuse_tangents("replay_logprob", logits, temperature)
     others = (temperature, packed_ids, lengths, tokens, capture_status, support_bits)
     out = _replay_forward(logits, *others, return_logprobs, stream)
     if logits.requires_grad and torch.is_grad_enabled():
+        if temperature.requires_grad:
+            warnings.warn("replay_logprob takes temperature as a constant: no gradient reaches it "
+                          "(detach it to say so)", stacklevel=2)
         return differentiable_replay(out, logits, others, stream)
     return out
 
