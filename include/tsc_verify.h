@@ -21,6 +21,12 @@
  * (token id / 4, 0, ...), the sampler's own: it is the token that tsc_sample_with_mask would
  * have drawn there. Equal scores go to the lowest id.
  *
+ * Scores are compared in float64 wherever they are close, so that the token does not depend on how
+ * a row is shared out. What they are computed from has its own precision: on logits, the sum of a
+ * row's softmax is held to about 2e-6, which scales p and q (it does not touch a draw from p alone,
+ * but u q(d) < p(d) and p - q may go either way that close to equality); on captures, the logprobs
+ * are the float32 ones that were captured.
+ *
  * If rounding leaves no token with p > q after a rejection (p and q agree within it), the
  * drafted token itself is emitted; it is not counted as accepted.
  */

@@ -68,7 +68,7 @@ int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 int32_t launched() { return hipGetLastError() == hipSuccess ? TSC_OK : TSC_ERR_HIP; }
 
 struct VerifyLayout {
-  int64_t parts, best, arrived, bytes;  // offsets, and the whole
+  int64_t parts, score, winner, arrived, bytes;  // offsets, and the whole
   int32_t rows;
   Cut stats, race;
 };
@@ -79,8 +79,9 @@ VerifyLayout verify_layout(int64_t N, int32_t K, int64_t V, bool has_draft) {
   l.stats = stats_cut(N * l.rows, V);
   l.race = race_cut(N, V);
   l.parts = 0;
-  l.best = N * l.rows * l.stats.n * (int64_t)sizeof(tsc::RowPart);
-  l.arrived = l.best + N * 8;
+  l.score = N * l.rows * l.stats.n * (int64_t)sizeof(tsc::RowPart);
+  l.winner = l.score + N * l.race.n * 8;
+  l.arrived = l.winner + N * l.race.n * 4;
   l.bytes = round16(l.arrived + N * 4);
   return l;
 }
@@ -257,7 +258,8 @@ int32_t tsc_verify_drafts(const void* target_logits, int32_t target_dtype, int64
                           target_dtype, draft_dtype, N, V, K, temperature, draft_temperature,
                           draft_tokens, draft_counts, uniforms, seeds, positions, tokens, accepted,
                           logprobs, row_status, reinterpret_cast<tsc::RowPart*>(ws + l.parts),
-                          reinterpret_cast<uint64_t*>(ws + l.best),
+                          reinterpret_cast<uint64_t*>(ws + l.score),
+                          reinterpret_cast<uint32_t*>(ws + l.winner),
                           reinterpret_cast<uint32_t*>(ws + l.arrived), l.rows, l.stats.n, l.race.n,
                           l.stats.len, l.race.len};
   (void)hipGetLastError();  // start from a clean error state so a launch error is ours

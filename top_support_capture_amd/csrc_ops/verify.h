@@ -36,7 +36,8 @@ struct VerifyArgs {
   int8_t* row_status; // [N]
   // Workspace.
   RowPart* parts;     // [N, rows, slices]
-  uint64_t* best;     // [N]: the best share's winner so far (see race_key)
+  uint64_t* score;    // [N, shares]: the score of each share's winner, the bits of a double
+  uint32_t* winner;   // [N, shares]: its id
   uint32_t* arrived;  // [N]: shares that are done
   int32_t rows;       // K + 1 target rows, then K draft rows when there is a draft distribution
   int32_t slices, shares;
@@ -49,12 +50,6 @@ struct RacePart {
   int32_t id;
   int32_t pad;
 };
-
-// A winner as one word that compares as it does: the score in float32, then the lower id. 0 when
-// nothing takes part.
-__device__ inline uint64_t race_key(RacePart b) {
-  return b.score > 0.0 ? (uint64_t)__float_as_uint((float)b.score) << 32 | (0xFFFFFFFFu - (uint32_t)b.id) : 0u;
-}
 
 __device__ inline RacePart better(RacePart a, RacePart b) {
   return b.score > a.score || (b.score == a.score && b.id < a.id) ? b : a;
@@ -73,7 +68,7 @@ __global__ void __launch_bounds__(kOpThreads) verify_stats_kernel(VerifyArgs a) 
   for (int64_t item = blockIdx.x; item < a.N * per; item += gridDim.x) {
     const int64_t n = item / per, rest = item - n * per;
     const int32_t r = (int32_t)(rest / a.slices), sl = (int32_t)(rest - (int64_t)r * a.slices);
-    if (rest == 0 && threadIdx.x == 0) a.arrived[n] = 0u, a.best[n] = 0u;
+    if (rest == 0 && threadIdx.x == 0) a.arrived[n] = 0u;
     const float T = a.temperature[n];
     const bool is_draft = r > a.K;
     const int32_t i = is_draft ? r - a.K - 1 : r;
@@ -146,10 +141,12 @@ __device__ inline float race_exponential(float t) {
   return t < 0.0625f ? series : -0.69314718f * __builtin_amdgcn_logf(1.0f - t);
 }
 
-// A race is run in float32 and decided in float64: each thread keeps its best entry by the
-// float32 score, and the threads whose score is within kRaceClose of the best one evaluate
-// theirs again in float64. (Two entries that close within one thread of the many are the
-// float32 score's to order.) float32 holds p and q to about 2e-6, exponents down to -40 rounded.
+__device__ inline double race_exponential_64(float t) { return -log1p(-(double)t); }
+
+// A race is run in float32 and decided in float64: each thread keeps its best entry, by the float32
+// scores where they are kRaceClose apart and by float64 ones where they are not, and the threads
+// whose score is within kRaceClose of the best one evaluate theirs in float64, as do the shares of
+// a request. float32 holds p and q to about 2e-6, exponents down to -40 rounded.
 // A difference p - q below p / 64 would keep too little of that: such a weight is evaluated in
 // float64. An entry comes that far only if the upper bound of its weight, (p - q) + p kRaceSlack,
 // can still win, which few entries' do.
@@ -171,7 +168,12 @@ struct RaceEntry {
     float w = p - q;
     if (race_near(p, w)) w = (float)exact(a_, b_);
     const float sc = w * __builtin_amdgcn_rcpf(race_exponential(tt));
-    if (sc > score || (sc == score && i < id)) score = sc, t = tt, a = a_, b = b_, id = i;
+    if (!(sc > score * (1.0f - kRaceClose))) return;
+    if (score > 0.0f && sc * (1.0f - kRaceClose) < score) {
+      const double mine = exact(a, b) / race_exponential_64(t), other = exact(a_, b_) / race_exponential_64(tt);
+      if (other < mine || (other == mine && id < i)) return;
+    }
+    score = sc, t = tt, a = a_, b = b_, id = i;
   }
   __device__ static inline bool race_near(float p, float w) { return __builtin_fabsf(w) < p * kRaceNear; }
   // E >= t: an entry whose largest possible w / t is no better than `bound` cannot win.
@@ -194,7 +196,7 @@ __device__ inline RacePart race_winner(const RaceEntry& e, Weight weight, float*
   RacePart b{0.0, INT32_MAX, 0};
   if (wave > 0.0f && wave >= top * (1.0f - kRaceClose)) {  // wave-uniform
     if (e.score > 0.0f && e.score >= top * (1.0f - kRaceClose)) {
-      const double sc = weight(e.a, e.b) / -log1p(-(double)e.t);
+      const double sc = weight(e.a, e.b) / race_exponential_64(e.t);
       if (sc > 0.0) b = {sc, e.id, 0};
     }
     const double best = wave_reduce(b.score, MaxOp());
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
   __shared__ uint32_t sh_bound;
   __shared__ float sh_score[kOpWaves];
   __shared__ RacePart sh_best[kOpWaves];
-  __shared__ uint64_t sh_key;
+  __shared__ int32_t sh_token;
   using TB = typename Row<TD>::Bits;
   using DB = typename Row<DD>::Bits;
   const int64_t n = blockIdx.x / a.shares;
@@ -461,26 +463,46 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
     race_chunk(at, x, y);
   }
   const RacePart won = race_winner<kOpWaves>(best, exact, sh_score, sh_best);
-  // The shares meet in two words of the request. Each thread 0 adds its winner, waits for the word's
-  // old value, and only then counts itself in, so that whoever counts last finds every winner in.
+  // The shares meet in the workspace. Each one's first thread puts its winner there, waits for the
+  // words' old values, and only then counts itself in, so that whoever counts last finds every
+  // winner in, and lets a lane look at each.
   // (Releasing and acquiring the whole memory at device scope instead, for plain stores of the
   // winners, took as long as the race: every workgroup wrote back and invalidated its L2.)
-  if (tid == 0) {
-    const uint64_t before =
-        __hip_atomic_fetch_max(&a.best[n], race_key(won), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    uint32_t one = 1u;
-    asm volatile("" : "+v"(one) : "v"((uint32_t)before), "v"((uint32_t)(before >> 32)));  // needs `before`
-    const uint32_t count = __hip_atomic_fetch_add(&a.arrived[n], one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sh_key = count != (uint32_t)a.shares - 1u
-                 ? ~uint64_t{0}
-                 : __hip_atomic_load(&a.best[n], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  constexpr int32_t kWait = -2, kNone = -1;
+  if (w == 0) {
+    uint32_t count = 0;
+    if (lane == 0) {
+      const int64_t at = n * a.shares + share;
+      const uint64_t before = __hip_atomic_exchange(&a.score[at], __builtin_bit_cast(uint64_t, won.score),
+                                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t other = __hip_atomic_exchange(&a.winner[at], (uint32_t)won.id, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT);
+      uint32_t one = 1u;  // needs both old values
+      asm volatile("" : "+v"(one) : "v"((uint32_t)before), "v"((uint32_t)(before >> 32)), "v"(other));
+      count = __hip_atomic_fetch_add(&a.arrived[n], one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    int32_t token = kWait;
+    if (__builtin_amdgcn_readfirstlane(count) == (uint32_t)a.shares - 1u) {
+      static_assert(kMaxSlices <= kWaveSize, "a lane a share");
+      double score = 0.0;
+      int32_t id = INT32_MAX;
+      if ((int32_t)lane < a.shares) {
+        const int64_t at = n * a.shares + lane;
+        score = __builtin_bit_cast(double, __hip_atomic_load(&a.score[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        id = (int32_t)__hip_atomic_load(&a.winner[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      const double top = wave_reduce(score, MaxOp());
+      id = wave_reduce(score == top ? id : INT32_MAX, MinOp());
+      token = top > 0.0 ? id : kNone;
+    }
+    if (lane == 0) sh_token = token;
   }
   lds_barrier();
-  const uint64_t key = sh_key;
-  if (key == ~uint64_t{0}) return;
+  const int32_t token = sh_token;
+  if (token == kWait) return;
   // No token with p > q: the two distributions agree within rounding, and the draft is as good a
   // draw from p as any.
-  finish(key != 0u ? (int32_t)(0xFFFFFFFFu - (uint32_t)key) : drafted);
+  finish(token != kNone ? token : drafted);
 }
 
 // ---- Over captured supports ---------------------------------------------------------------------
