@@ -43,3 +43,26 @@ def test_replay_allocates_on_its_stream(allocations):
     assert len(allocations) == 3 and all(a == s for a in allocations)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_sampler_and_csr_allocate_on_their_stream(allocations):
+    log("case sampler and CSR allocate on the stream that they are given")
+    rng = np.random.default_rng(4)
+    x, _ = logits(rng, (4, 300), "bf16")
+    full = lambda v, dt=torch.float32: torch.full((4,), v, dtype=dt, device=DEV)
+    keys = torch.arange(4, device=DEV)
+    args = (x, full(0.9), full(0, torch.int32), full(1.0), full(0.0), keys.int(), keys, keys, 8)
+    want = tsc.sample_with_mask(*args, return_bits=True)
+    csr = tsc.support_csr(want)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del allocations[:]
+    got = tsc.sample_with_mask(*args, return_bits=True, stream=s)
+    again = tsc.support_csr(got, stream=s)
+    # Six outputs and the bitmasks, which are cleared on that stream too, before the sampler writes
+    # them; three of the CSR.
+    assert len(allocations) == 10 and all(a == s for a in allocations)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want) if a.dim() == 1 or a.dtype == torch.uint8)
+    n = int(csr.offsets[-1])
+    assert torch.equal(again.offsets, csr.offsets) and torch.equal(again.ids[:n], csr.ids[:n])

@@ -224,16 +224,17 @@ class PreparedSample:
         _check(positions, "positions", torch.int64, B, dev)
         if out is None:
             Wc = max(int(W), 1)
-            out = SampleOutput(
-                tokens=torch.empty(B, dtype=torch.int32, device=dev),
-                packed_ids=torch.empty((R, Wc), dtype=torch.int32, device=dev),
-                lengths=torch.empty(R, dtype=torch.int32, device=dev),
-                logprobs=(torch.empty((R, Wc), dtype=torch.float32, device=dev)
-                          if return_logprobs else None),
-                selected_logprob=torch.empty(R, dtype=torch.float32, device=dev),
-                row_status=torch.empty(B, dtype=torch.int8, device=dev),
-                support_bits=(torch.zeros((R, support_bits_ld(V)), dtype=torch.uint8, device=dev)
-                              if return_bits else None))
+            with _on(stream):  # the bitmasks are cleared there, before the sampler writes them
+                out = SampleOutput(
+                    tokens=torch.empty(B, dtype=torch.int32, device=dev),
+                    packed_ids=torch.empty((R, Wc), dtype=torch.int32, device=dev),
+                    lengths=torch.empty(R, dtype=torch.int32, device=dev),
+                    logprobs=(torch.empty((R, Wc), dtype=torch.float32, device=dev)
+                              if return_logprobs else None),
+                    selected_logprob=torch.empty(R, dtype=torch.float32, device=dev),
+                    row_status=torch.empty(B, dtype=torch.int8, device=dev),
+                    support_bits=(torch.zeros((R, support_bits_ld(V)), dtype=torch.uint8, device=dev)
+                                  if return_bits else None))
         else:
             _check_out(out, B, R, W, dev)
             sb = out.support_bits
@@ -388,10 +389,11 @@ def support_csr(out: SampleOutput, cap: Optional[int] = None,
     R, W = out.packed_ids.shape
     dev = out.packed_ids.device
     cap = R * W if cap is None else int(cap)
-    csr = SupportCsr(torch.empty(R + 1, dtype=torch.int64, device=dev),
-                     torch.empty(max(cap, 1), dtype=torch.int32, device=dev),
-                     torch.empty(max(cap, 1), dtype=torch.float32, device=dev)
-                     if out.logprobs is not None else None)
+    with _on(stream):
+        csr = SupportCsr(torch.empty(R + 1, dtype=torch.int64, device=dev),
+                         torch.empty(max(cap, 1), dtype=torch.int32, device=dev),
+                         torch.empty(max(cap, 1), dtype=torch.float32, device=dev)
+                         if out.logprobs is not None else None)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     code = lib.tsc_support_csr(_ptr(out.lengths), _ptr(out.packed_ids), _ptr(out.logprobs), R, W,
                                csr.offsets.data_ptr(), csr.ids.data_ptr(), _ptr(csr.logprobs),
