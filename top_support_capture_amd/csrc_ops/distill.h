@@ -64,7 +64,7 @@ __device__ inline bool distill_row_read(const DistillArgs& a, int64_t n) {
   if (!empty && len > 0 && len <= a.W && temperature_ok(a.temperature[n]) &&
       (a.teacher_temperature == nullptr || temperature_ok(a.teacher_temperature[n])))
     return true;
-  if (threadIdx.x == 0 && a.loss != nullptr) {
+  if (threadIdx.x == 0) {
     a.loss[n] = empty ? 0.0f : __builtin_nanf("");
     a.row_status[n] = (int8_t)(empty ? TSC_ROW_NO_SUPPORT : TSC_ROW_INVALID_PARAM);
   }
@@ -250,20 +250,19 @@ struct GradStream {
   __device__ inline void ask(int j, int k) {
     if (lo + 8 <= hi) v[j] = Row<DT>::load_once(row + (place(k) + 8 <= hi ? place(k) : lo));
   }
-  __device__ inline void start(int k0) {
+  __device__ inline void start() {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) ask(j, k0 + j);
+    for (int j = 0; j < kAhead; ++j) ask(j, j);
   }
-  // Windows k0 and on, after start(k0). add(k) adds the entries of window k; k0's are in place.
-  template <class Add>
-  __device__ inline void run(int k0, const Entries<kThr>& ent, Add add, float m, float c, float g_s) {
-    for (; lo + (int64_t)k0 * kSize < hi; k0 += kAhead) {
+  // All windows, after start(); the entries of the first are in place.
+  __device__ inline void run(const Entries<kThr>& ent, float m, float c, float g_s) {
+    for (int k0 = 0; lo + (int64_t)k0 * kSize < hi; k0 += kAhead) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int k = k0 + j;
         const int64_t at = place(k);
         if (lo + (int64_t)k * kSize < hi) {  // uniform
-          ent.turn(k, add, [&] {
+          ent.turn(k, [&](int next) { ent.add(next); }, [&] {
             if (at < hi) {
               float x[8], p[8];
               if (at + 8 <= hi)
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kGradThreads, 8) distill_grad_kernel(DistillAr
   TeacherEntries<DT, kGradThreads> t;
   t.load(a, n, len, (int32_t)threadIdx.x);
   GradStream<DT, kGradThreads> stream{row, out, lo, hi};
-  stream.start(0);
+  stream.start();
   ent.begin();
   lds_barrier();
   visit_entries<DT, kGradThreads>(a, n, len, t, lo, hi, [&](uint32_t at, float) { ent.count(at); });
@@ -318,10 +317,9 @@ __global__ void __launch_bounds__(kGradThreads, 8) distill_grad_kernel(DistillAr
     ent.place(at, exp2_scaled(value - r.vm, ct) * minus_g_A);
   });
   lds_barrier();
-  auto add = [&](int k) { ent.add(k, [](float p) { return p; }); };
-  add(0);
+  ent.add(0);
   lds_barrier();
-  stream.run(0, ent, add, r.m, c, g / r.s);
+  stream.run(ent, r.m, c, g / r.s);
 }
 
 // Loss and gradient, a row per workgroup: the row is read twice, but the second time soon after
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(kGradThreads, 8) distill_fused_kernel(DistillA
     return;
   }
   GradStream<DT, kGradThreads> stream{row, out, 0, a.V};
-  stream.start(0);
+  stream.start();
   visit_entries<DT, kGradThreads>(a, n, len, t, 0, a.V, [&](uint32_t at, float) { ent.count(at); });
   lds_barrier();
   ent.offsets();
@@ -365,10 +363,9 @@ __global__ void __launch_bounds__(kGradThreads, 8) distill_fused_kernel(DistillA
     ent.place(at, exp2_scaled(value - r.vm, ct) * minus_g_A);
   });
   lds_barrier();
-  auto add = [&](int k) { ent.add(k, [](float p) { return p; }); };
-  add(0);
+  ent.add(0);
   lds_barrier();
-  stream.run(0, ent, add, r.m, c, g / r.s);
+  stream.run(ent, r.m, c, g / r.s);
 }
 
 }  // namespace tsc

@@ -122,7 +122,7 @@ int64_t distill_bytes(int64_t N, int64_t V) {
   return cut.n > 1 ? N * cut.n * (int64_t)sizeof(tsc::RowPart) : 0;
 }
 
-// Checks that the distillation's entry points share; TSC_OK with *empty set when there is no row.
+// Checks that the distillation's and the replay gradient's entry points share.
 int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld, int32_t W) {
   if (!dtype_ok(dtype) || N < 0 || V < 1 || V > kMaxVocab || ld < V || W < 1)
     return TSC_ERR_INVALID_ARGUMENT;
@@ -254,10 +254,10 @@ int32_t tsc_verify_drafts(const void* target_logits, int32_t target_dtype, int64
   if (const int32_t e = check_workspace(workspace, workspace_bytes, l.bytes)) return e;
   char* ws = static_cast<char*>(workspace);
   const tsc::VerifyArgs a{target_logits, target_stride_n, target_stride_k,
-                          K > 0 ? draft_logits : nullptr, draft_stride_n, draft_stride_k,
-                          target_dtype, draft_dtype, N, V, K, temperature, draft_temperature,
-                          draft_tokens, draft_counts, uniforms, seeds, positions, tokens, accepted,
-                          logprobs, row_status, reinterpret_cast<tsc::RowPart*>(ws + l.parts),
+                          K > 0 ? draft_logits : nullptr, draft_stride_n, draft_stride_k, N, V, K,
+                          temperature, draft_temperature, draft_tokens, draft_counts, uniforms, seeds,
+                          positions, tokens, accepted, logprobs, row_status,
+                          reinterpret_cast<tsc::RowPart*>(ws + l.parts),
                           reinterpret_cast<uint64_t*>(ws + l.score),
                           reinterpret_cast<uint32_t*>(ws + l.winner),
                           reinterpret_cast<uint32_t*>(ws + l.arrived), l.rows, l.stats.n, l.race.n,

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
           flags |= 1u;
       }
     }
-    streamed = block_all<kGradWaves>(again, [](uint32_t p, uint32_t q) { return p | q; }, sh.f) == 0u;
+    streamed = block_all(again, [](uint32_t p, uint32_t q) { return p | q; }, sh.f) == 0u;
   }
   const bool entries = !streamed || (gl != nullptr && len_ok);  // the packed ids take part
 
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kGradThreads, kStreams ? 4 : 8) replay_grad_ke
   lds_barrier();
   constexpr int kSize = Window<kGradThreads>::kSize;
   auto add = [&](int k) {
-    ent.add(k, [](float v) { return v; });
+    ent.add(k);
     if (tid == 0 && tok >= lo && tok < hi && (tok - lo) / kSize == k)
       ent.at_window(k).add((uint32_t)((tok - lo) % kSize), gs * inv_T);
   };

@@ -189,42 +189,29 @@ __device__ inline float wave_max(float v) {
 // hold one entry each.
 template <int kW, class C>
 __device__ inline void block_lse(float& m, double& s, C c, float* sh_m, double* sh_s) {
-  static_assert(kW <= 8 || kW == 16, "a loop over the waves, or one row of 16 lanes");
   const uint32_t w = threadIdx.x / kWaveSize, lane = threadIdx.x & (kWaveSize - 1);
   const float wm = wave_max(m);
   const double ws = wave_reduce(rescaled(s, m, wm, c), SumOp());
   if (lane == 0) sh_m[w] = wm, sh_s[w] = ws;
   lds_barrier();
-  if constexpr (kW == 16) {
-    const float om = sh_m[lane & 15];
-    m = row16_reduce(om, [](float p, float q) { return __builtin_fmaxf(p, q); });
-    s = row16_reduce(rescaled(sh_s[lane & 15], om, m, c), SumOp());
-  } else {
-    float M = sh_m[0];
+  float M = sh_m[0];
 #pragma unroll
-    for (int i = 1; i < kW; ++i) M = __builtin_fmaxf(M, sh_m[i]);
-    double S = 0.0;
+  for (int i = 1; i < kW; ++i) M = __builtin_fmaxf(M, sh_m[i]);
+  double S = 0.0;
 #pragma unroll
-    for (int i = 0; i < kW; ++i) S += rescaled(sh_s[i], sh_m[i], M, c);
-    m = M, s = S;
-  }
+  for (int i = 0; i < kW; ++i) S += rescaled(sh_s[i], sh_m[i], M, c);
+  m = M, s = S;
 }
 
-// A value over the workgroup under op, the same for every thread; sh holds one entry per wave.
-template <int kW, class T, class Op>
+// A value over a workgroup of 16 waves under op, the same for every thread; sh holds one entry per
+// wave.
+template <class T, class Op>
 __device__ inline T block_all(T v, Op op, T* sh) {
   v = wave_reduce(v, op);
   lds_barrier();  // sh may still be read by an earlier call
   if ((threadIdx.x & (kWaveSize - 1)) == 0) sh[threadIdx.x / kWaveSize] = v;
   lds_barrier();
-  if constexpr (kW == 16) {
-    return row16_reduce(sh[threadIdx.x & 15], op);
-  } else {
-    v = sh[0];
-#pragma unroll
-    for (int i = 1; i < kW; ++i) v = op(v, sh[i]);
-    return v;
-  }
+  return row16_reduce(sh[threadIdx.x & 15], op);
 }
 
 // ---- Writing a row with a few scattered entries --------------------------------------------------
@@ -323,23 +310,22 @@ struct Entries {
     val[i] = v, rel[i] = (uint16_t)(at % kSize);
   }
   __device__ inline Window<kThr> at_window(int k) const { return {window + (two ? (k & 1) * kSize : 0)}; }
-  // Window k's turn: use() takes its chunks; add(k + 1) adds the entries of the next.
-  template <class Add, class Use>
-  __device__ inline void turn(int k, Add add, Use use) const {
-    if (two) add(k + 1);
+  // Window k's turn: use() takes its chunks; put(k + 1) adds the entries of the next.
+  template <class Put, class Use>
+  __device__ inline void turn(int k, Put put, Use use) const {
+    if (two) put(k + 1);
     use();
     lds_barrier();
     if (!two) {
-      add(k + 1);
+      put(k + 1);
       lds_barrier();
     }
   }
-  // The entries of window k (none past the last), each through term(value).
-  template <class Term>
-  __device__ inline void add(int k, Term term) const {
+  // The entries of window k (none past the last).
+  __device__ inline void add(int k) const {
     if (k >= kMaxWindows) return;
     const Window<kThr> win = at_window(k);
-    for (uint32_t i = start[k] + threadIdx.x; i < start[k + 1]; i += kThr) win.add(rel[i], term(val[i]));
+    for (uint32_t i = start[k] + threadIdx.x; i < start[k + 1]; i += kThr) win.add(rel[i], val[i]);
   }
 };
 

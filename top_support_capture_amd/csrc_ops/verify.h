@@ -20,7 +20,6 @@ struct VerifyArgs {
   int64_t t_sn, t_sk;  // strides in elements
   const void* draft;   // [N, K, V] or null: drafts without a distribution (q is 1 at the draft)
   int64_t d_sn, d_sk;
-  int32_t t_dtype, d_dtype;
   int64_t N, V;
   int32_t K;
   const float* temperature;        // [N]
@@ -482,7 +481,7 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
       count = __hip_atomic_fetch_add(&a.arrived[n], one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     int32_t token = kWait;
-    if (__builtin_amdgcn_readfirstlane(count) == (uint32_t)a.shares - 1u) {
+    if ((uint32_t)__builtin_amdgcn_readfirstlane(count) == (uint32_t)a.shares - 1u) {
       static_assert(kMaxSlices <= kWaveSize, "a lane a share");
       double score = 0.0;
       int32_t id = INT32_MAX;
