@@ -1,4 +1,4 @@
-"""Where the calls that take a stream allocate and run (needs an MI355X)."""
+"""Where the calls that take a stream allocate and run, and what their errors name (needs an MI355X)."""
 import numpy as np
 import pytest
 import torch
@@ -66,3 +66,14 @@ def test_sampler_and_csr_allocate_on_their_stream(allocations):
     assert all(torch.equal(a, b) for a, b in zip(got, want) if a.dim() == 1 or a.dtype == torch.uint8)
     n = int(csr.offsets[-1])
     assert torch.equal(again.offsets, csr.offsets) and torch.equal(again.ids[:n], csr.ids[:n])
+
+
+def test_errors_name_their_call():
+    # Packed rows of width 0, which the library refuses before any launch.
+    log("case errors of the replay and the CSR name them")
+    i = dict(dtype=torch.int32, device=DEV)
+    x, one, ids, n = torch.zeros(2, 8, device=DEV), torch.ones(2, device=DEV), torch.zeros(2, 0, **i), torch.zeros(2, **i)
+    with pytest.raises(tsc.TscError, match="tsc_replay_logprob failed: TSC_ERR_INVALID_ARGUMENT"):
+        tsc.replay_logprob(x, one, ids, n, n)
+    with pytest.raises(tsc.TscError, match="tsc_support_csr failed: TSC_ERR_INVALID_ARGUMENT"):
+        tsc.support_csr(tsc.SampleOutput(n, ids, n, None, one, n.char()))

@@ -371,7 +371,7 @@ def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_st
 
     out, code = _launch(dev, stream, go)
     if code != 0:
-        raise TscError(code, lib.tsc_status_string(code).decode())
+        raise TscError(code, lib.tsc_status_string(code).decode(), "tsc_replay_logprob")
     return out
 
 
@@ -399,7 +399,7 @@ def support_csr(out: SampleOutput, cap: Optional[int] = None,
                                csr.offsets.data_ptr(), csr.ids.data_ptr(), _ptr(csr.logprobs),
                                cap, s.cuda_stream)
     if code != 0:
-        raise TscError(code, lib.tsc_status_string(code).decode())
+        raise TscError(code, lib.tsc_status_string(code).decode(), "tsc_support_csr")
     return csr
 
 
