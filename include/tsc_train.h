@@ -28,7 +28,8 @@ extern "C" {
  * N, V         0 <= N <= 2^21, 1 <= V < 2^31 - 16, and N ceil(V / 2^19) <= 2^21.
  * temperature  [N] float32, normal positive finite.
  * teacher_ids, teacher_values [N, W] int32 and float32: entries past lengths[n] are not read. Ids
- *              in [0, V); an id that occurs twice counts twice. A value of -inf has probability 0.
+ *              in [0, V); an id that occurs twice counts twice (of three and more, the gradient's
+ *              float32 terms are added in no fixed order). A value of -inf has probability 0.
  * lengths      [N] int32 in [0, W]; a row of length 0 has loss 0, no gradient and status
  *              TSC_ROW_NO_SUPPORT, and its logits are not read (padding).
  * W            1..TSC_MAX_PACKED_WIDTH.
@@ -82,8 +83,10 @@ size_t tsc_distill_topk_grad_workspace(int64_t N, int64_t V);
  * the support logprob of packed id i plus, at the row's token, that of the selected logprob:
  *     grad_logits[n, j] = (G_j - pi_j sum_{i in S} G_i) / T   for j in S, 0 elsewhere.
  *
- * logits .. tokens  as given to tsc_replay_logprob. The packed ids of a row are distinct (one that
- *              occurs twice counts twice, as it does there).
+ * logits .. tokens  as given to tsc_replay_logprob, with N <= 2^21 and N ceil(V / 2^19) <= 2^21 (more
+ *              rows are TSC_ERR_UNSUPPORTED here). The packed ids of a row are distinct (one that
+ *              occurs twice counts twice, as it does there; the float32 terms of one that occurs
+ *              oftener, or twice at the token, are added in no fixed order).
  * grad_selected [N] float32 or NULL (0): upstream gradient of selected_logprob. It has no effect
  *              on a row whose token is not in its support (whose logprob is -inf).
  * grad_logprobs [N, W] float32 or NULL (0): upstream gradient of logprobs; entries past lengths[n]

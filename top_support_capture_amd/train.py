@@ -2,7 +2,9 @@
 
 ``distill_topk`` is differentiable with respect to the student's logits, and so is
 ``replay_logprob``. The backward passes run on the stream that the forward ran on, allocate the
-gradient, and synchronise nothing. Captured into a HIP graph, a backward pass needs leaves that no
+gradient, and synchronise nothing. With ``stream`` given, the inputs have to be ready there, and a
+tensor of another stream that is freed before the work is done needs ``record_stream``, as with any
+torch operator on a side stream. Captured into a HIP graph, a backward pass needs leaves that no
 eager graph still holds: torch's engine would accumulate into those outside the capture."""
 from __future__ import annotations
 

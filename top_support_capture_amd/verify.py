@@ -2,8 +2,8 @@
 
 ``verify_drafts`` works on both models' logits, ``verify_captured`` on the supports that
 ``sample_with_mask`` captured for them. Both run asynchronously on the current stream (or
-``stream``), allocate their outputs on the inputs' device and can be captured in a HIP graph. Their
-outputs have no derivatives."""
+``stream``, where the inputs have to be ready), allocate their outputs on the inputs' device and can
+be captured in a HIP graph. Their outputs have no derivatives."""
 from __future__ import annotations
 
 from typing import NamedTuple, Optional, Tuple
