@@ -183,9 +183,9 @@ __device__ inline DistillRow distill_row(const DistillArgs& a, int64_t n,
 }
 
 // The loss, a row per workgroup. With one slice to a row the workgroup reads the row itself: 1024
-// rows of 151936 bfloat16 logits take 65 us, 4.9 TB/s with the teacher's entries, the rate at which
-// HBM is read. (Slices for 256-thread workgroups and a second launch: 109 us.) 64 float32 rows of
-// 32000: 8.3 us, one row's latency.
+// rows of 151936 bfloat16 logits take 66 us, 4.9 TB/s with the teacher's entries, where a bare read
+// reaches 6.1. (Slices for 256-thread workgroups and a second launch: 109 us.) 64 float32 rows of
+// 32000: 8.5 us, one row's latency.
 constexpr int kLossThreads = 1024;
 
 template <int DT>
@@ -281,8 +281,8 @@ struct GradStream {
   }
 };
 
-// The gradient of a segment of a row per workgroup: a row is read once and written once, 103 us for
-// 1024 rows of 151936 bfloat16 logits (6.05 TB/s, HBM). Entries added to the finished row instead
+// The gradient of a segment of a row per workgroup: a row is read once and written once, 104 us for
+// 1024 rows of 151936 bfloat16 logits (6.0 TB/s behind the L2). Entries added to the finished row instead
 // took 185 us.
 template <int DT>
 __global__ void __launch_bounds__(kGradThreads, 8) distill_grad_kernel(DistillArgs a) {

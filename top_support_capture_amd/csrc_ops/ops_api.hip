@@ -44,7 +44,8 @@ Cut cut_rows(int64_t rows, int64_t V, int64_t unit, int64_t most, int64_t target
 Cut stats_cut(int64_t rows, int64_t V) { return cut_rows(rows, V, 2048, 32768, 2048); }
 // The distillation's loss: rows enough for the chip, or short ones, are read by one workgroup each,
 // which saves a launch and the merge (bf16, 1024 rows of 151936 65 us against 82 + 27 in slices, 200
-// rows 20.0 against 17.1 + 8.6, 64 rows 17.4 against 9.0 + 7.8).
+// rows 20.0 against 17.1 + 8.6, 64 rows 17.4 against 9.0 + 7.8; 128 rows 17.5 against 19.0; float32,
+// 128 rows of 151936 19.4 against 23.3, of 262144 37.7 against 33.5, 200 rows of those 49.7 against 49.3).
 Cut loss_cut(int64_t N, int64_t V) {
   return N >= 128 || V <= 65536 ? Cut{1, V} : stats_cut(N, V);
 }
@@ -174,7 +175,9 @@ hipError_t launch_distill_grad(const tsc::DistillArgs& a, int32_t dtype, hipStre
 
 // One workgroup per row for loss and gradient together, when there are rows enough or they are
 // short; one launch instead of two or three. (bf16, W = 2048, of which half is used: 256 rows of
-// 151936 take 42 us against 48 and a launch, 1024 rows 160 against 170; 64 rows 35 against 30.)
+// 151936 take 42 us against 48 and a launch, 1024 rows 160 against 170; 64 rows 35 against 30. 128
+// rows 35 against 37 in slices and segments; float32, 128 rows of 151936 51 against 57, of 262144 86
+// against 83, 200 rows of those 119 against 129.)
 bool fused(int64_t N, int64_t V) { return V <= tsc::kMaxSegment && (N >= 128 || V <= 65536); }
 
 // The fused kernel's second reading of a row comes from the last-level cache (256 MB), if the rows

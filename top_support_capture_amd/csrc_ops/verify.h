@@ -55,9 +55,10 @@ __device__ inline RacePart better(RacePart a, RacePart b) {
 }
 
 // Softmax statistics of each row's slices; greedy requests take the maximum's place of each
-// target row instead and read no draft row. Bound by HBM: 64 requests of 4 drafts over 151936
-// bfloat16 logits, 175 MB, take 36 us (4.8 TB/s); 4 to 8 waves a SIMD, slices of 16384 to 100000
-// elements and fewer vector instructions all measure the same. (One request: 4.3 us.)
+// target row instead and read no draft row. Bound by reading: 64 requests of 4 drafts over 151936
+// bfloat16 logits, 175 MB, take 36 us (4.8 TB/s; a bare read in workgroups of this size 34 us); 4 to
+// 8 waves a SIMD, slices of 16384 to 100000 elements and fewer vector instructions all measure the
+// same. (One request: 4.4 us.)
 template <int TD, int DD>
 __global__ void __launch_bounds__(kOpThreads) verify_stats_kernel(VerifyArgs a) {
   __shared__ float sh_m[kOpWaves];
@@ -235,10 +236,11 @@ __device__ inline Decision first_stop(const int32_t* code, int32_t count, int32_
   return {stop, code[stop]};
 }
 
-// The race at the position where a request stops. On a batch it is bound by Philox and the weights,
-// about 1300 cycles of a SIMD for 512 elements: 27 us for 64 requests over 151936 logits; for one
-// request by a chain of dependent steps, 12 us. Requests are shared out so that there are about 512
-// workgroups (384, 640, 768 and 1024: 30.6, 29.9, 27.8 and 27.8 us against 28.0).
+// The race at the position where a request stops: 28 us for 64 requests over 151936 logits, 13 us for
+// one request. Philox and the weights, about 1300 cycles of a SIMD for 512 elements, are 10 us of the
+// batch's; the rest of both is a chain of dependent steps (merge and decision 5 and 4 us, first loads
+// 1, winner 2, the shares' meeting 1) and, on a batch, uneven shares. Requests are shared out so that
+// there are about 512 workgroups (384, 640, 768 and 1024: 30.6, 29.9, 27.8 and 27.8 us against 28.0).
 template <int TD, int DD>
 __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a) {
   __shared__ RowPart tp[kMaxDrafts + 1], dp[kMaxDrafts];
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kOpThreads, 4) verify_race_kernel(VerifyArgs a
 // lists, all positions at once; at the position where the request stops, the drafter's list goes
 // into a hash table in LDS that the target's entries look themselves up in, and race. A few
 // megabytes move; the time is that of the chain of lookup, decision, table and race: 9 us for
-// supports of 64, 15 us for 256 requests of 4 drafts with supports of up to 2048, and for 64 of 2
+// supports of 64, 15 us for 256 requests of 4 drafts with supports of up to 2048, 16 us for 64 of 2
 // with up to 8192.
 struct SupportArgs {
   const int32_t* ids;      // slot i of request n at (n * sn + i * sk) * W
