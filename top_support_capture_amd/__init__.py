@@ -152,7 +152,7 @@ def _logits_dtype(t: torch.Tensor, name: str) -> int:
 def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], go):
     """``go(handle)`` with ``dev`` and ``stream`` (default: its current stream) current, for the
     launch and the allocations around it; the usual case costs no context switch."""
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == torch._C._cuda_getDevice():  # a tensor there: initialised
         return go(torch._C._cuda_getCurrentRawStream(dev.index))
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream must be on {dev}")
@@ -165,9 +165,8 @@ def _on(stream: Optional[torch.cuda.Stream]):
 
 
 def _refuse_tangents(call: str, *tensors: Optional[torch.Tensor]) -> None:
-    """The derivatives are reverse-mode ones: the tangent of a dual tensor would be lost in silence."""
-    if forward_ad._current_level < 0:  # outside any dual level, which costs next to nothing to see
-        return
+    """The derivatives are reverse-mode ones: the tangent of a dual tensor would be lost in silence.
+    Called only within a dual level: outside there are no dual tensors."""
     if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise NotImplementedError(f"{call} has no forward-mode derivative")
 
@@ -317,7 +316,8 @@ def replay_logprob(logits: torch.Tensor, temperature: torch.Tensor, packed_ids: 
     and to nothing else: ``temperature`` is taken as a constant (with a warning if it asks for a gradient
     that would not reach it). With ``stream`` given, their backward
     pass runs there too. There is no forward-mode derivative: dual tensors are refused."""
-    _refuse_tangents("replay_logprob", logits, temperature)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("replay_logprob", logits, temperature)
     others = (temperature, packed_ids, lengths, tokens, capture_status, support_bits)
     out = _replay_forward(logits, *others, return_logprobs, stream)
     if logits.requires_grad and torch.is_grad_enabled():
@@ -333,11 +333,9 @@ def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_st
     lib = library()
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [N, V] with unit column stride")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("logits must be float32 or bfloat16")
-    dt = TSC_DTYPE_BF16 if logits.dtype == torch.bfloat16 else TSC_DTYPE_F32
+    dt = _logits_dtype(logits, "logits")
     dev = logits.device
-    if dev.type != "cuda":
+    if not logits.is_cuda:
         raise ValueError("logits must be on a GPU")
     N, V = logits.shape
     ld = logits.stride(0) if N > 1 else V
@@ -347,7 +345,7 @@ def _replay_forward(logits, temperature, packed_ids, lengths, tokens, capture_st
     if (packed_ids.device != dev or packed_ids.dtype != torch.int32 or packed_ids.dim() != 2
             or packed_ids.shape[0] != N or not packed_ids.is_contiguous()):
         raise ValueError(f"packed_ids must be a contiguous int32 tensor [{N}, W] on {dev}")
-    W = int(packed_ids.shape[1])
+    W = packed_ids.shape[1]
     if capture_status is not None:
         _check(capture_status, "capture_status", torch.int8, N, dev)
     bits_ld = 0

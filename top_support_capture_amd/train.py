@@ -11,6 +11,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import TscError, _check, _launch, _logits_dtype, _on, _ptr, _refuse_tangents, library
@@ -146,7 +147,8 @@ class _Distill(torch.autograd.Function):
     def backward(ctx, grad_loss):
         if grad_loss is None:
             return None, None, None
-        _refuse_tangents("the gradient of distill_topk", grad_loss)
+        if forward_ad._current_level >= 0:
+            _refuse_tangents("the gradient of distill_topk", grad_loss)
         go = _distill_backward_once if torch.is_grad_enabled() else _distill_backward
         return go(ctx, grad_loss)
 
@@ -164,7 +166,8 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     The loss is differentiable with respect to ``logits``, in reverse mode: dual tensors are refused.
     Weight or average the rows with torch; when the weights are known beforehand,
     ``distill_topk_grad`` gives loss and gradient in one call."""
-    _refuse_tangents("distill_topk", logits, teacher_values, temperature, teacher_temperature)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("distill_topk", logits, teacher_values, temperature, teacher_temperature)
     if torch.is_grad_enabled():
         _refuse_other_gradients(teacher_values, temperature, teacher_temperature)
     others = (teacher_ids, teacher_values, lengths, temperature, teacher_temperature)
@@ -182,8 +185,9 @@ def distill_topk_grad(logits: torch.Tensor, teacher_ids: torch.Tensor,
                       stream: Optional[torch.cuda.Stream] = None) -> DistillGradOutput:
     """The losses of ``distill_topk`` and the gradient of sum(row_weights * loss) with respect to
     ``logits``, in one call and without autograd. ``row_weights``: float32 [N]."""
-    _refuse_tangents("distill_topk_grad", logits, teacher_values, temperature, teacher_temperature,
-                     row_weights)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("distill_topk_grad", logits, teacher_values, temperature, teacher_temperature,
+                         row_weights)
     lib = library()
     args, dev = _distill_args(logits, teacher_ids, teacher_values, lengths, temperature,
                               teacher_temperature)
@@ -217,7 +221,8 @@ def replay_logprob_backward(logits: torch.Tensor, temperature: torch.Tensor,
     upstream gradients of its ``selected_logprob`` and ``logprobs`` (None: 0; entries past each
     length are not read). Rows whose replay status is not ROW_OK have gradient 0. This is the
     call that autograd makes; made directly it needs no graph of torch's."""
-    _refuse_tangents("replay_logprob_backward", logits, temperature, grad_selected, grad_logprobs)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("replay_logprob_backward", logits, temperature, grad_selected, grad_logprobs)
     dt, N, V, ld, dev = _rows(logits)
     W = _packed(packed_ids, "packed_ids", torch.int32, N, None, dev)
     _check(temperature, "temperature", torch.float32, N, dev)
@@ -276,7 +281,8 @@ class _Replay(torch.autograd.Function):
     def backward(ctx, grad_selected, grad_logprobs=None):
         if grad_selected is None and grad_logprobs is None:
             return None, None, None
-        _refuse_tangents("the gradient of replay_logprob", grad_selected, grad_logprobs)
+        if forward_ad._current_level >= 0:
+            _refuse_tangents("the gradient of replay_logprob", grad_selected, grad_logprobs)
         go = _replay_backward_once if torch.is_grad_enabled() else _replay_backward
         return go(ctx, grad_selected, grad_logprobs)
 
