@@ -2,7 +2,9 @@
 
 Python binding of the C-ABI library ``libtsc.so`` (declared in ``include/tsc.h``; the verification
 of drafted tokens in ``include/tsc_verify.h`` and ``verify.py``, training over captured supports
-in ``include/tsc_train.h`` and ``train.py``). This module
+in ``include/tsc_train.h`` and ``train.py``, logprobs under the whole softmax in
+``include/tsc_logprob.h`` and ``logprob.py``, gradient clipping in ``include/tsc_clip.h`` and
+``clip.py``). This module
 only marshals arguments: it checks tensor devices and dtypes, allocates the output tensors with
 PyTorch on the logits' device, and calls ``tsc_sample_with_mask`` on the current HIP stream.
 Every step of the sampling runs in the library's HIP kernels; there is no fallback, and the
@@ -28,7 +30,10 @@ __all__ = ["sample_with_mask", "prepare", "PreparedSample", "SampleOutput", "wor
            "MAX_PACKED_WIDTH", "TscError",
            "verify_drafts", "verify_captured", "VerifyOutput", "Support", "support_of",
            "MAX_DRAFTS", "distill_topk", "DistillOutput", "distill_topk_grad",
-           "DistillGradOutput", "replay_logprob_backward"]
+           "DistillGradOutput", "replay_logprob_backward",
+           "token_logprobs", "TokenLogprobsOutput", "token_logprobs_grad",
+           "TokenLogprobsGradOutput", "MAX_TOP",
+           "grad_norm", "clip_grad_norm", "clip_grads", "prepare_grads", "PreparedGrads"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtsc.so")
 
@@ -88,14 +93,28 @@ def library() -> ctypes.CDLL:
     lib.tsc_distill_topk_grad.argtypes = distill + [P, P, P, P, P, SZ, P]
     lib.tsc_replay_logprob_backward.argtypes = [P, I32, I64, I64, I64, P, P, P, I32, P, P, I64, P,
                                                 P, P, P, P]
+    rows = [P, I32, I64, I64, I64, P, P]
+    lib.tsc_token_logprobs.argtypes = rows + [I32, P, P, P, P, P, P, P, SZ, P]
+    lib.tsc_token_logprobs_backward.argtypes = rows + [P, I32] + [P] * 6
+    lib.tsc_token_logprobs_grad.argtypes = rows + [P] * 7 + [SZ, P]
+    tensors = [P, P, P, I64]
+    lib.tsc_grad_norm.argtypes = tensors + [P, P, SZ, P]
+    lib.tsc_clip_grad_norm.argtypes = tensors + [P, P, ctypes.c_float, P, P, SZ, P]
+    lib.tsc_clip_grads.argtypes = tensors + [P, P, ctypes.c_float, P, P]
     for f in (lib.tsc_verify_drafts, lib.tsc_verify_captured, lib.tsc_distill_topk,
               lib.tsc_distill_topk_backward, lib.tsc_distill_topk_grad,
-              lib.tsc_replay_logprob_backward):
+              lib.tsc_replay_logprob_backward, lib.tsc_token_logprobs,
+              lib.tsc_token_logprobs_backward, lib.tsc_token_logprobs_grad, lib.tsc_grad_norm,
+              lib.tsc_clip_grad_norm, lib.tsc_clip_grads):
         f.restype = I32
     lib.tsc_distill_topk_workspace.argtypes = [I64, I64]
     lib.tsc_distill_topk_grad_workspace.argtypes = [I64, I64]
+    lib.tsc_token_logprobs_workspace.argtypes = [I64, I64, I32]
+    lib.tsc_token_logprobs_grad_workspace.argtypes = [I64, I64]
+    lib.tsc_grad_norm_workspace.argtypes = [I64]
     for f in (lib.tsc_verify_drafts_workspace, lib.tsc_distill_topk_workspace,
-              lib.tsc_distill_topk_grad_workspace):
+              lib.tsc_distill_topk_grad_workspace, lib.tsc_token_logprobs_workspace,
+              lib.tsc_token_logprobs_grad_workspace, lib.tsc_grad_norm_workspace):
         f.restype = SZ
     _lib = lib
     return lib
@@ -412,6 +431,9 @@ def csr_to_host(csr: SupportCsr, stream: Optional[torch.cuda.Stream] = None):
     return offsets.numpy(), ids, lps
 
 
+from .clip import (PreparedGrads, clip_grad_norm, clip_grads, grad_norm, prepare_grads)  # noqa: E402
+from .logprob import (MAX_TOP, TokenLogprobsGradOutput, TokenLogprobsOutput, token_logprobs,  # noqa: E402
+                      token_logprobs_grad)
 from .train import (DistillGradOutput, DistillOutput, differentiable_replay, distill_topk,  # noqa: E402
                     distill_topk_grad, replay_logprob_backward)
 from .verify import (MAX_DRAFTS, Support, VerifyOutput, support_of, verify_captured,  # noqa: E402

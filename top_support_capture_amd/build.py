@@ -1,5 +1,5 @@
 """Build the HIP library ``libtsc.so`` in-tree for gfx950 with hipcc: the sampler's translation
-unit (``csrc/``) and that of the operators around it (``csrc_ops/``), compiled side by side.
+unit (``csrc/``) and those of the operators around it (``csrc_ops/``), compiled side by side.
 
 ``python -m top_support_capture_amd.build`` (or ``build()``) always recompiles. The library is
 placed next to this file, where the Python binding loads it.
@@ -15,7 +15,9 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "tsc_api.hip"),
-           os.path.join(HERE, "csrc_ops", "ops_api.hip")]
+           os.path.join(HERE, "csrc_ops", "ops_api.hip"),
+           os.path.join(HERE, "csrc_ops", "logprob_api.hip"),
+           os.path.join(HERE, "csrc_ops", "clip_api.hip")]
 LIB = os.path.join(HERE, "libtsc.so")
 ARCH = os.environ.get("TSC_OFFLOAD_ARCH", "gfx950")
 

@@ -1,0 +1,204 @@
+// Host side of the C ABI declared in include/tsc_clip.h: argument validation and kernel launches on
+// the caller's stream. Nothing here allocates device memory or synchronizes.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "clip.h"
+#include "host_common.h"
+#include "tsc_clip.h"
+
+namespace {
+
+constexpr int64_t kMaxTensors = int64_t{1} << 20;
+constexpr int64_t kMaxElements = int64_t{1} << 40;
+// Up to so many partial sums every workgroup of the scaling adds up by itself, which saves a launch.
+constexpr int64_t kJoinInline = 4 * tsc::kClipGroups;
+
+int64_t size_of(int32_t dtype) { return dtype == TSC_DTYPE_F32 ? 4 : 2; }
+
+int32_t check_list(const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int64_t count) {
+  if (count < 0 || (count > 0 && (!tensors || !numels || !dtypes))) return TSC_ERR_INVALID_ARGUMENT;
+  if (count > kMaxTensors) return TSC_ERR_UNSUPPORTED;
+  int64_t all = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (!dtype_ok(dtypes[i]) || numels[i] < 0) return TSC_ERR_INVALID_ARGUMENT;
+    if (numels[i] >= kMaxElements || (all += numels[i]) >= kMaxElements) return TSC_ERR_UNSUPPORTED;
+    if (numels[i] > 0 && (!tensors[i] || !aligned(tensors[i], dtypes[i])))
+      return TSC_ERR_INVALID_ARGUMENT;
+  }
+  return TSC_OK;
+}
+
+struct Lists {
+  const void* const* src;
+  const int64_t* numels;
+  const int32_t* dtypes;
+  int64_t count;
+  void* const* dst;  // null: in place
+  const int32_t* dst_dtypes;
+  uintptr_t begin(int64_t i) const { return reinterpret_cast<uintptr_t>(src[i]); }
+  uintptr_t end(int64_t i) const { return begin(i) + (uintptr_t)(numels[i] * size_of(dtypes[i])); }
+  uintptr_t out_begin(int64_t i) const { return dst ? reinterpret_cast<uintptr_t>(dst[i]) : begin(i); }
+  int32_t out_dtype(int64_t i) const { return dst ? dst_dtypes[i] : dtypes[i]; }
+  uintptr_t out_end(int64_t i) const { return out_begin(i) + (uintptr_t)(numels[i] * size_of(out_dtype(i))); }
+  bool own(int64_t i) const { return out_begin(i) == begin(i) && out_dtype(i) == dtypes[i]; }
+};
+
+// Results that no other result and no gradient but their own overlaps.
+int32_t check_out(const Lists& l) {
+  if ((l.dst == nullptr) != (l.dst_dtypes == nullptr)) return TSC_ERR_INVALID_ARGUMENT;
+  if (l.dst) {
+    if (const int32_t e = check_list(const_cast<const void* const*>(l.dst), l.numels, l.dst_dtypes, l.count)) return e;
+  }
+  std::vector<std::pair<uintptr_t, uintptr_t>> written;
+  written.reserve((size_t)l.count);
+  bool sorted = true;
+  for (int64_t i = 0; i < l.count; ++i) {
+    if (l.numels[i] == 0) continue;
+    if (!written.empty() && l.out_begin(i) < written.back().first) sorted = false;
+    written.emplace_back(l.out_begin(i), l.out_end(i));
+  }
+  if (!sorted) std::sort(written.begin(), written.end());
+  for (size_t i = 1; i < written.size(); ++i)
+    if (written[i].first < written[i - 1].second) return TSC_ERR_INVALID_ARGUMENT;
+  if (!l.dst) return TSC_OK;
+  for (int64_t i = 0; i < l.count; ++i) {
+    if (l.numels[i] == 0 || l.own(i)) continue;
+    // The first result that ends behind the gradient's begin.
+    const auto at = std::upper_bound(written.begin(), written.end(), l.begin(i),
+                                     [](uintptr_t b, const auto& w) { return b < w.second; });
+    if (at != written.end() && at->first < l.end(i)) return TSC_ERR_INVALID_ARGUMENT;
+  }
+  return TSC_OK;
+}
+
+// Tensors [from, ...) into an empty table, as many as fit; returns the index behind them. The
+// tensors' addresses and types are the caller's to add.
+template <class Table, class Add>
+int64_t fill(Table& t, const Lists& l, int64_t from, Add add) {
+  t.n = 0;
+  t.first[0] = 0;
+  int64_t i = from;
+  for (; i < l.count && t.n < Table::kSize; ++i) {
+    const int64_t units = ceil_div(l.numels[i], tsc::kClipUnit);
+    if (units == 0) continue;
+    t.src[t.n] = l.src[i];
+    t.numel[t.n] = l.numels[i];
+    if (l.dtypes[i] == TSC_DTYPE_F32) t.f32[t.n >> 5] |= 1u << (t.n & 31);
+    add(t.n, i);
+    t.first[t.n + 1] = t.first[t.n] + (uint32_t)units;
+    ++t.n;
+  }
+  return i;
+}
+
+template <class Table>
+unsigned groups(const Table& t) { return t.first[t.n] < (uint32_t)tsc::kClipGroups ? t.first[t.n] : (unsigned)tsc::kClipGroups; }
+
+// Launches the sums; returns how many partial sums they leave.
+int64_t launch_norm(const Lists& l, double* partials, hipStream_t s) {
+  int64_t n = 0;
+  for (int64_t i = 0; i < l.count;) {
+    tsc::NormTable t{};
+    i = fill(t, l, i, [](int32_t, int64_t) {});
+    if (t.n == 0) break;
+    hipLaunchKernelGGL(tsc::clip_norm_kernel, dim3(groups(t)), dim3(tsc::kClipThreads), 0, s, t, partials + n);
+    n += groups(t);
+  }
+  return n;
+}
+
+void launch_join(const double* partials, int64_t n, float* norm, hipStream_t s) {
+  hipLaunchKernelGGL(tsc::clip_join_kernel, dim3(1), dim3(tsc::kClipThreads), 0, s, partials, (int32_t)n, norm);
+}
+
+void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
+  c.in_place = 1;
+  for (int64_t i = 0; i < l.count; ++i)
+    if (l.numels[i] > 0 && !l.own(i)) c.in_place = 0;
+  // Tables of up to kSize tensors, the last ones first: the norm's pass has read those last.
+  for (int64_t end = l.count; end > 0;) {
+    const int64_t from = end > tsc::ScaleTable::kSize ? end - tsc::ScaleTable::kSize : 0;
+    Lists part = l;
+    part.count = end;
+    tsc::ScaleTable t{};
+    fill(t, part, from, [&](int32_t k, int64_t i) {
+      t.dst[k] = reinterpret_cast<void*>(l.out_begin(i));
+      if (l.out_dtype(i) == TSC_DTYPE_F32) t.dst_f32[k >> 5] |= 1u << (k & 31);
+    });
+    if (t.n > 0) {
+      hipLaunchKernelGGL(tsc::clip_scale_kernel, dim3(groups(t)), dim3(tsc::kClipThreads), 0, s, t, c);
+      c.norm_out = nullptr;  // written once
+    }
+    end = from;
+  }
+}
+
+int32_t check_norm(float* norm, int64_t count, const void* workspace, size_t have) {
+  if (!norm) return TSC_ERR_INVALID_ARGUMENT;
+  return check_workspace(workspace, have, (int64_t)tsc_grad_norm_workspace(count));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tsc_grad_norm_workspace(int64_t count) {
+  if (count < 1 || count > kMaxTensors) return 0;
+  return (size_t)(ceil_div(count, tsc::NormTable::kSize) * tsc::kClipGroups) * sizeof(double);
+}
+
+int32_t tsc_grad_norm(const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int64_t count,
+                      float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int32_t e = check_list(tensors, numels, dtypes, count)) return e;
+  if (const int32_t e = check_norm(norm, count, workspace, workspace_bytes)) return e;
+  (void)hipGetLastError();  // start from a clean error state so a launch error is ours
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  double* partials = static_cast<double*>(workspace);
+  const int64_t n = launch_norm({tensors, numels, dtypes, count, nullptr, nullptr}, partials, s);
+  launch_join(partials, n, norm, s);
+  return launched();
+}
+
+int32_t tsc_clip_grad_norm(const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int64_t count,
+                           void* const* out, const int32_t* out_dtypes, float max_norm, float* norm, void* workspace,
+                           size_t workspace_bytes, void* stream) try {
+  if (const int32_t e = check_list(tensors, numels, dtypes, count)) return e;
+  if (!(max_norm >= 0.0f)) return TSC_ERR_INVALID_ARGUMENT;
+  const Lists l{tensors, numels, dtypes, count, out, out_dtypes};
+  if (const int32_t e = check_out(l)) return e;
+  if (const int32_t e = check_norm(norm, count, workspace, workspace_bytes)) return e;
+  (void)hipGetLastError();
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  double* partials = static_cast<double*>(workspace);
+  const int64_t n = launch_norm(l, partials, s);
+  if (n == 0 || n > kJoinInline) {
+    launch_join(partials, n, norm, s);
+    launch_scale(l, {nullptr, 0, nullptr, norm, max_norm, 0}, s);
+  } else {
+    launch_scale(l, {partials, (int32_t)n, norm, nullptr, max_norm, 0}, s);
+  }
+  return launched();
+} catch (const std::bad_alloc&) {
+  return TSC_ERR_INVALID_ARGUMENT;
+}
+
+int32_t tsc_clip_grads(const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int64_t count,
+                       void* const* out, const int32_t* out_dtypes, float max_norm, const float* norm,
+                       void* stream) try {
+  if (const int32_t e = check_list(tensors, numels, dtypes, count)) return e;
+  if (!(max_norm >= 0.0f) || !norm) return TSC_ERR_INVALID_ARGUMENT;
+  const Lists l{tensors, numels, dtypes, count, out, out_dtypes};
+  if (const int32_t e = check_out(l)) return e;
+  (void)hipGetLastError();
+  launch_scale(l, {nullptr, 0, nullptr, norm, max_norm, 0}, reinterpret_cast<hipStream_t>(stream));
+  return launched();
+} catch (const std::bad_alloc&) {
+  return TSC_ERR_INVALID_ARGUMENT;
+}
+
+}  // extern "C"

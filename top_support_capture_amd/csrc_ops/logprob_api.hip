@@ -1,0 +1,206 @@
+// Host side of the C ABI declared in include/tsc_logprob.h: argument validation and kernel launches
+// on the caller's stream. Nothing here allocates device memory or synchronizes; scratch memory is
+// the caller's workspace.
+#include <hip/hip_runtime.h>
+
+#include "host_common.h"
+#include "logprob.h"
+#include "tsc_logprob.h"
+
+namespace {
+
+static_assert(TSC_MAX_TOP == tsc::kTopMost, "the selection's lists hold that many");
+
+// Whole rows for a workgroup each when there are rows enough, or short ones; slices otherwise.
+Cut pass_cut(int64_t N, int64_t V) {
+  return N >= 128 || V <= 65536 ? Cut{1, V} : cut_rows(N, V, tsc::kTopRound, 4 * tsc::kTopRound, 512);
+}
+
+// The gradient: segments of 16384 elements, longer ones only to bound the grid.
+Cut segment_cut(int64_t N, int64_t V) {
+  int64_t len = 16384;
+  while (len < tsc::kMaxSegment && N * ceil_div(V, len) > (int64_t{1} << 22)) len *= 2;
+  return {(int32_t)ceil_div(V, len), len};
+}
+
+int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld) {
+  if (!dtype_ok(dtype) || N < 0 || V < 1 || V > kMaxVocab || ld < V) return TSC_ERR_INVALID_ARGUMENT;
+  if (N > kMaxRows || N * ceil_div(V, tsc::kMaxSegment) > kMaxRows) return TSC_ERR_UNSUPPORTED;
+  if (N > 0 && (!logits || !aligned(logits, dtype))) return TSC_ERR_INVALID_ARGUMENT;
+  return TSC_OK;
+}
+
+int64_t parts_bytes(int64_t N, const Cut& cut) {
+  return cut.n > 1 ? round16(N * cut.n * (int64_t)sizeof(tsc::LogprobPart)) : 0;
+}
+
+int64_t pass_bytes(int64_t N, int64_t V, int32_t top) {
+  const Cut cut = pass_cut(N, V);
+  return cut.n > 1 ? parts_bytes(N, cut) + round16(N * cut.n * top * 8) : 0;
+}
+
+// Slices' states and keys from `ws` on.
+void set_parts(tsc::LogprobArgs& a, char* ws) {
+  const Cut cut = pass_cut(a.N, a.V);
+  a.slices = cut.n, a.slice_len = cut.len;
+  a.parts = reinterpret_cast<tsc::LogprobPart*>(ws);
+  a.keys = reinterpret_cast<uint64_t*>(ws + parts_bytes(a.N, cut));
+}
+
+template <class Kernel>
+hipError_t launch_top(Kernel kernel, const tsc::LogprobArgs& a, int64_t groups, unsigned threads, bool top,
+                      std::atomic<uint64_t>& allowed, hipStream_t s) {
+  if (top) {
+    const hipError_t err = allow_lds(kernel, tsc::kTopLds, allowed);
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), top ? tsc::kTopLds : 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, bool kEnt, bool kTop>
+hipError_t launch_pass(const tsc::LogprobArgs& a, hipStream_t s) {
+  static std::atomic<uint64_t> whole{0}, slice{0}, join{0};
+  if (a.slices == 1)
+    return launch_top(&tsc::logprob_kernel<DT, kEnt, kTop>, a, a.N, tsc::kTopThreads, kTop, whole, s);
+  const hipError_t err =
+      launch_top(&tsc::logprob_slice_kernel<DT, kEnt, kTop>, a, a.N * a.slices, tsc::kTopThreads, kTop, slice, s);
+  if (err != hipSuccess) return err;
+  return launch_top(&tsc::logprob_join_kernel<DT, kEnt, kTop>, a, a.N, kTop ? tsc::kTopThreads : tsc::kWaveSize, kTop,
+                    join, s);
+}
+
+hipError_t launch_pass(const tsc::LogprobArgs& a, int32_t dtype, bool entropy, hipStream_t s) {
+  constexpr int F = TSC_DTYPE_F32, B = TSC_DTYPE_BF16;
+  if (dtype == F) {
+    if (entropy) return a.top ? launch_pass<F, true, true>(a, s) : launch_pass<F, true, false>(a, s);
+    return a.top ? launch_pass<F, false, true>(a, s) : launch_pass<F, false, false>(a, s);
+  }
+  if (entropy) return a.top ? launch_pass<B, true, true>(a, s) : launch_pass<B, true, false>(a, s);
+  return a.top ? launch_pass<B, false, true>(a, s) : launch_pass<B, false, false>(a, s);
+}
+
+template <int DT>
+void launch_grad(const tsc::LogprobArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.N * a.segments)), block(tsc::kLogprobGradThreads);
+  if (a.grad_top)
+    hipLaunchKernelGGL((tsc::logprob_grad_kernel<DT, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((tsc::logprob_grad_kernel<DT, false>), grid, block, 0, s, a);
+}
+
+hipError_t launch_grad(tsc::LogprobArgs& a, int32_t dtype, hipStream_t s) {
+  const Cut cut = segment_cut(a.N, a.V);
+  a.segments = cut.n, a.seg_len = cut.len;
+  dtype == TSC_DTYPE_F32 ? launch_grad<TSC_DTYPE_F32>(a, s) : launch_grad<TSC_DTYPE_BF16>(a, s);
+  return hipGetLastError();
+}
+
+// One workgroup per row for values and gradient together, when there are rows enough or they are
+// short; one launch instead of two or three.
+bool fused(int64_t N, int64_t V) { return N >= 128 || V <= 65536; }
+
+// The fused kernel's second reading of a row comes from the last-level cache (256 MB), if the rows
+// of all resident workgroups fit there: past kCached bytes of rows one workgroup is kept to a CU,
+// by asking for more than half of its LDS.
+constexpr int64_t kCached = 180 << 20;
+constexpr size_t kAlone = 84 * 1024;
+
+template <int DT, bool kEnt>
+hipError_t launch_fused(const tsc::LogprobArgs& a, hipStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  const auto kernel = &tsc::logprob_fused_kernel<DT, kEnt>;
+  const int64_t rows = (a.N < 512 ? a.N : 512) * a.V * (DT == TSC_DTYPE_F32 ? 4 : 2);
+  const hipError_t err = allow_lds(kernel, kAlone, allowed);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)a.N), dim3(tsc::kTopThreads), rows > kCached ? kAlone : 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_fused(const tsc::LogprobArgs& a, int32_t dtype, bool entropy, hipStream_t s) {
+  if (dtype == TSC_DTYPE_F32)
+    return entropy ? launch_fused<TSC_DTYPE_F32, true>(a, s) : launch_fused<TSC_DTYPE_F32, false>(a, s);
+  return entropy ? launch_fused<TSC_DTYPE_BF16, true>(a, s) : launch_fused<TSC_DTYPE_BF16, false>(a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tsc_token_logprobs_workspace(int64_t N, int64_t V, int32_t top) {
+  if (N < 1 || N > kMaxRows || V < 1 || V > kMaxVocab || top < 0 || top > TSC_MAX_TOP) return 0;
+  return (size_t)pass_bytes(N, V, top);
+}
+
+int32_t tsc_token_logprobs(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld,
+                           const float* temperature, const int32_t* tokens, int32_t top, float* logprobs,
+                           float* entropy, int32_t* top_ids, float* top_logprobs, int8_t* row_status, float* stats,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld)) return e;
+  if (top < 0 || top > V) return TSC_ERR_INVALID_ARGUMENT;
+  if (top > TSC_MAX_TOP) return TSC_ERR_UNSUPPORTED;
+  if (N == 0) return TSC_OK;
+  if (!tokens || !logprobs || !row_status || (top > 0 && (!top_ids || !top_logprobs))) return TSC_ERR_INVALID_ARGUMENT;
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, pass_bytes(N, V, top))) return e;
+  tsc::LogprobArgs a{};
+  a.logits = logits, a.N = N, a.V = V, a.ld = ld, a.temperature = temperature, a.tokens = tokens, a.top = top;
+  a.logprobs = logprobs, a.entropy = entropy, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
+  a.row_status = row_status, a.stats = stats;
+  set_parts(a, static_cast<char*>(workspace));
+  (void)hipGetLastError();  // start from a clean error state so a launch error is ours
+  return launch_pass(a, dtype, entropy != nullptr, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? TSC_OK
+                                                                                                       : TSC_ERR_HIP;
+}
+
+int32_t tsc_token_logprobs_backward(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld,
+                                    const float* temperature, const int32_t* tokens, const float* stats, int32_t top,
+                                    const int32_t* top_ids, const float* grad_logprobs, const float* grad_entropy,
+                                    const float* grad_top, void* grad_logits, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld)) return e;
+  if (top < 0 || top > V) return TSC_ERR_INVALID_ARGUMENT;
+  if (top > TSC_MAX_TOP) return TSC_ERR_UNSUPPORTED;
+  if (N == 0) return TSC_OK;
+  if (!tokens || !stats || !grad_logits || !aligned(grad_logits, dtype) || (top > 0 && grad_top && !top_ids))
+    return TSC_ERR_INVALID_ARGUMENT;
+  tsc::LogprobArgs a{};
+  a.logits = logits, a.N = N, a.V = V, a.ld = ld, a.temperature = temperature, a.tokens = tokens, a.top = top;
+  a.top_ids = const_cast<int32_t*>(top_ids), a.stats = const_cast<float*>(stats);
+  a.grad_logprobs = grad_logprobs, a.grad_entropy = grad_entropy, a.grad_top = top > 0 ? grad_top : nullptr;
+  a.grad = grad_logits;
+  (void)hipGetLastError();
+  return launch_grad(a, dtype, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? TSC_OK : TSC_ERR_HIP;
+}
+
+// Slices' states, a row's statistics, and room for entropies that the caller does not take.
+size_t tsc_token_logprobs_grad_workspace(int64_t N, int64_t V) {
+  if (N < 1 || N > kMaxRows || V < 1 || V > kMaxVocab || fused(N, V)) return 0;
+  return (size_t)(pass_bytes(N, V, 0) + N * 16 + round16(N * 4));
+}
+
+int32_t tsc_token_logprobs_grad(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld,
+                                const float* temperature, const int32_t* tokens, const float* grad_logprobs,
+                                const float* grad_entropy, float* logprobs, float* entropy, int8_t* row_status,
+                                void* grad_logits, void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int32_t e = check_rows(logits, dtype, N, V, ld)) return e;
+  if (N == 0) return TSC_OK;
+  if (!tokens || !grad_logprobs || !logprobs || !row_status || !grad_logits || !aligned(grad_logits, dtype))
+    return TSC_ERR_INVALID_ARGUMENT;
+  if (const int32_t e = check_workspace(workspace, workspace_bytes, (int64_t)tsc_token_logprobs_grad_workspace(N, V)))
+    return e;
+  tsc::LogprobArgs a{};
+  a.logits = logits, a.N = N, a.V = V, a.ld = ld, a.temperature = temperature, a.tokens = tokens;
+  a.logprobs = logprobs, a.entropy = entropy, a.row_status = row_status;
+  a.grad_logprobs = grad_logprobs, a.grad_entropy = grad_entropy, a.grad = grad_logits;
+  (void)hipGetLastError();
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const bool with_entropy = entropy || grad_entropy;
+  if (fused(N, V)) return launch_fused(a, dtype, with_entropy, s) == hipSuccess ? TSC_OK : TSC_ERR_HIP;
+  char* ws = static_cast<char*>(workspace);
+  set_parts(a, ws);
+  a.stats = reinterpret_cast<float*>(ws + pass_bytes(N, V, 0));
+  if (grad_entropy && !entropy) a.entropy = a.stats + N * 4;
+  if (launch_pass(a, dtype, with_entropy, s) != hipSuccess) return TSC_ERR_HIP;
+  return launch_grad(a, dtype, s) == hipSuccess ? TSC_OK : TSC_ERR_HIP;
+}
+
+}  // extern "C"

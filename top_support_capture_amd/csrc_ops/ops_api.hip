@@ -6,39 +6,13 @@
 #include <atomic>
 
 #include "distill.h"
+#include "host_common.h"
 #include "replay_grad.h"
 #include "tsc_train.h"
 #include "tsc_verify.h"
 #include "verify.h"
 
 namespace {
-
-constexpr int64_t kMaxRows = int64_t{1} << 21;  // one workgroup per row: 2^21 * 1024 threads fit a grid
-constexpr int64_t kMaxVocab = INT32_MAX - 16;
-
-bool dtype_ok(int32_t dtype) { return dtype == TSC_DTYPE_F32 || dtype == TSC_DTYPE_BF16; }
-
-bool aligned(const void* p, int32_t dtype) {
-  return reinterpret_cast<uintptr_t>(p) % (dtype == TSC_DTYPE_F32 ? 4 : 2) == 0;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct Cut {
-  int32_t n;
-  int64_t len;  // a multiple of `unit`
-};
-
-// `rows` rows of V elements cut into slices: enough slices for `target` workgroups in all, at
-// most kMaxSlices a row, none shorter than `unit` or, unless V asks for it, longer than `most`.
-Cut cut_rows(int64_t rows, int64_t V, int64_t unit, int64_t most, int64_t target) {
-  int64_t n = ceil_div(target, rows > 0 ? rows : 1);
-  if (n < ceil_div(V, most)) n = ceil_div(V, most);
-  if (n > ceil_div(V, unit)) n = ceil_div(V, unit);
-  if (n > tsc::kMaxSlices) n = tsc::kMaxSlices;
-  const int64_t len = ceil_div(ceil_div(V, n), unit) * unit;
-  return {(int32_t)ceil_div(V, len), len};
-}
 
 // Statistics of rows: slices of 32768 elements, or shorter ones until there are 2048 workgroups.
 Cut stats_cut(int64_t rows, int64_t V) { return cut_rows(rows, V, 2048, 32768, 2048); }
@@ -61,12 +35,6 @@ Cut grad_cut(int64_t N, int64_t V, int64_t target) {
 }
 // Races: see verify_race_kernel.
 Cut race_cut(int64_t N, int64_t V) { return cut_rows(N, V, 2048, 1 << 30, 512); }
-
-unsigned grid_of(int64_t items) { return (unsigned)(items < kMaxRows ? items : kMaxRows); }
-
-int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
-
-int32_t launched() { return hipGetLastError() == hipSuccess ? TSC_OK : TSC_ERR_HIP; }
 
 struct VerifyLayout {
   int64_t parts, score, winner, arrived, bytes;  // offsets, and the whole
@@ -95,23 +63,6 @@ void launch_verify(const tsc::VerifyArgs& a, hipStream_t s) {
                      dim3(tsc::kOpThreads), 0, s, a);
 }
 
-// The dynamic LDS limit of a kernel is a per-device attribute, set once per device.
-constexpr int kMaxDevices = 64;
-
-// Lets `kernel` have up to `bytes` of dynamic LDS on the current device.
-template <class Kernel>
-hipError_t allow_lds(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  hipError_t err = hipGetDevice(&dev);
-  if (err != hipSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-  if ((done.load(std::memory_order_acquire) >> dev) & 1u) return hipSuccess;
-  err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err == hipSuccess) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
-  return err;
-}
-
 uint32_t table_slots(int32_t W) {  // a power of two, at least twice the entries
   uint32_t n = 64;
   while (n < 2u * (uint32_t)W) n <<= 1;
@@ -131,13 +82,6 @@ int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int6
   if (N > kMaxRows || W > TSC_MAX_PACKED_WIDTH || N * ceil_div(V, tsc::kMaxSegment) > kMaxRows)
     return TSC_ERR_UNSUPPORTED;
   if (N > 0 && (!logits || !aligned(logits, dtype))) return TSC_ERR_INVALID_ARGUMENT;
-  return TSC_OK;
-}
-
-int32_t check_workspace(const void* workspace, size_t have, int64_t need) {
-  if (have < (size_t)need) return TSC_ERR_WORKSPACE;
-  if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
-    return TSC_ERR_INVALID_ARGUMENT;
   return TSC_OK;
 }
 
