@@ -146,7 +146,7 @@ def test_overlaps_are_refused(lib, which, kw):
 def test_clip_workspaces(lib):
     size = lib.tsc_grad_norm_workspace
     assert size(0) == size(-1) == size(2**20 + 1) == 0
-    assert 0 < size(1) <= size(184) < size(185) and size(1) % 16 == 0
+    assert 0 < size(1) <= size(304) < size(305) and size(1) % 16 == 0
 
 
 # ---- Python --------------------------------------------------------------------------------------------

@@ -20,6 +20,8 @@ Tensors = Union[torch.Tensor, Iterable[torch.Tensor]]
 
 def _dense(t: torch.Tensor) -> bool:
     """Whether the elements lie one behind the other in some order of the dimensions."""
+    if t.numel() == 0:
+        return True
     want = 1
     for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
         if stride != want:
@@ -36,13 +38,13 @@ def _listed(tensors: Tensors, name: str):
     except (KeyError, AttributeError):
         raise ValueError(f"{name} must be float32 or bfloat16 tensors") from None
     dev = tensors[0].device if tensors else None
-    for t in tensors:
-        if t.device != dev or dev.type != "cuda":
-            raise ValueError(f"{name} must be on one GPU")
-        if t.layout is not torch.strided or not (t.is_contiguous() or t.numel() == 0 or _dense(t)):
-            raise ValueError(f"{name} must be dense: without gaps or elements that share their place")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} must not ask for gradients (detach them): the norm and the clipping have none")
+    if any(t.device != dev for t in tensors) or (tensors and dev.type != "cuda"):
+        raise ValueError(f"{name} must be on one GPU")
+    if (any(t.layout is not torch.strided for t in tensors)
+            or not (all(map(torch.Tensor.is_contiguous, tensors)) or all(map(_dense, tensors)))):
+        raise ValueError(f"{name} must be dense: without gaps or elements that share their place")
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise ValueError(f"{name} must not ask for gradients (detach them): the norm and the clipping have none")
     return tensors, dtypes
 
 
@@ -79,6 +81,7 @@ class PreparedGrads:
         self._list = (at(self._ptrs), at(self._numels), at(self._dtypes), len(self.tensors))
         self._results = (at(self._out_ptrs), at(self._out_dtypes))
         self._nbytes = self._lib.tsc_grad_norm_workspace(len(self.tensors))
+        self._versions = self.tensors if self.out is None else self.out  # what is marked as changed
 
     def _refuse(self, call: str, *more) -> None:
         if forward_ad._current_level >= 0:
@@ -87,9 +90,6 @@ class PreparedGrads:
     def _norm_and_workspace(self):
         return (torch.empty((), dtype=torch.float32, device=self._dev),
                 torch.empty(self._nbytes, dtype=torch.uint8, device=self._dev) if self._nbytes else None)
-
-    def _written(self) -> None:
-        torch.autograd.graph.increment_version(self.tensors if self.out is None else self.out)
 
     def norm(self, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """As ``grad_norm``."""
@@ -116,7 +116,7 @@ class PreparedGrads:
             return norm
 
         norm = _launch(self._dev, stream, go)
-        self._written()
+        torch.autograd.graph.increment_version(self._versions)
         return norm
 
     def scale(self, norm: torch.Tensor, max_norm: float, stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -131,14 +131,18 @@ class PreparedGrads:
             _raise(self._lib, code, "tsc_clip_grads")
 
         _launch(self._dev, stream, go)
-        self._written()
+        torch.autograd.graph.increment_version(self._versions)
 
 
 def prepare_grads(tensors: Tensors, out: Optional[Tensors] = None) -> PreparedGrads:
     """Check a list of gradients once, for programs whose gradients stay where they are from step to
     step: the returned object's ``norm()``, ``clip(max_norm)`` and ``scale(norm, max_norm)`` are
     ``grad_norm``, ``clip_grad_norm`` and ``clip_grads`` of these tensors."""
-    return PreparedGrads(tensors, out)
+    plan = PreparedGrads(tensors, out)
+    # Views of a tensor share its version: one of them is enough.
+    bases = {id(t if t._base is None else t._base): t for t in plan._versions}
+    plan._versions = tuple(bases.values())
+    return plan
 
 
 def grad_norm(tensors: Tensors, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:

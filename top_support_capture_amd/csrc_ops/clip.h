@@ -1,102 +1,115 @@
 // The norm of many tensors taken together, and tensors scaled down to a norm.
 //
 // A launch covers up to a table of tensors, which travels in the kernel's arguments: nothing is
-// copied to the device beforehand, and a captured launch keeps its table. The tensors' elements,
-// cut into units of kClipUnit, are dealt to the workgroups in one contiguous span each, whatever
-// the tensors' sizes.
+// copied to the device beforehand, and a captured launch keeps its table. The tensors' elements are
+// cut into units, numbered through the table, and dealt to the workgroups in turn, so that what is
+// in flight lies close together in memory.
 #pragma once
 
-#include "row_stats.h"
+#include "piece.h"
 
 namespace tsc {
 
-constexpr int kClipThreads = 512;
+constexpr int kClipThreads = 256;
 constexpr int kClipWaves = kClipThreads / kWaveSize;
-constexpr int64_t kClipUnit = kClipThreads * 8;  // elements
-constexpr int kClipGroups = 1024;                // at most, of one launch
-constexpr int kClipInFlight = 4;                 // chunks of 8 elements a thread
+constexpr int kClipGroups = 2048;  // of a norm's launch, at most: 8 workgroups on each CU
 
-// kN tensors, the table's size bounded by the 4 KB that a kernel's arguments may take.
-template <int kN>
+// Up to kN tensors in units of kUnit elements. kN is bounded by the 4 KB that a kernel's arguments
+// may take: a tensor's address, type and the size of its last unit share a word.
+template <int kN, int kUnit, bool kOut>
 struct ClipTable {
   static constexpr int kSize = kN;
-  const void* src[kN];
-  int64_t numel[kN];
-  uint32_t first[kN + 1];  // units before each tensor; the last: all
-  uint32_t f32[(kN + 31) / 32];
+  static constexpr int64_t kUnitSize = kUnit;
+  static constexpr int kHints = 32;
+  static_assert(kUnit <= 8192, "13 bits of the word");
+  uint64_t src[kN];
+  uint64_t dst[kOut ? kN : 1];  // the address and the type
+  uint32_t first[kN + 1];       // units before each tensor; the last: all
+  uint32_t hint[kHints];        // the tensor of unit i << hint_shift (whole words: scalar loads)
+  uint32_t units, hint_shift;
   int32_t n;
-  __device__ inline bool is_f32(int t) const { return (f32[t >> 5] >> (t & 31)) & 1u; }
-};
 
-template <int kN>
-struct ClipOutTable : ClipTable<kN> {
-  void* dst[kN];
-  uint32_t dst_f32[(kN + 31) / 32];
-  __device__ inline bool to_f32(int t) const { return (dst_f32[t >> 5] >> (t & 31)) & 1u; }
-};
-
-using NormTable = ClipTable<184>;
-using ScaleTable = ClipOutTable<136>;
-
-// visit(t, lo, hi) for the parts of tensors in this workgroup's span of units, in order or from
-// the last to the first.
-template <bool kBackwards, class Table, class Visit>
-__device__ inline void visit_span(const Table& a, Visit visit) {
-  const uint32_t units = a.first[a.n];
-  uint32_t u0 = (uint32_t)((uint64_t)blockIdx.x * units / gridDim.x);
-  uint32_t u1 = (uint32_t)((uint64_t)(blockIdx.x + 1) * units / gridDim.x);
-  if (u0 == u1) return;
-  const uint32_t at = kBackwards ? u1 - 1 : u0;
-  int t = 0;  // the last tensor that begins at or before unit `at`
-  for (int below = a.n; below - t > 1;) {
-    const int mid = (t + below) >> 1;
-    if (a.first[mid] <= at) t = mid;
-    else below = mid;
-  }
-  while (u0 < u1) {
-    const uint32_t b = a.first[t], e = a.first[t + 1];
-    const uint32_t lo = u0 > b ? u0 : b, hi = u1 < e ? u1 : e;
-    if (lo < hi) {
-      const int64_t end = (int64_t)(hi - b) * kClipUnit;
-      visit(t, (int64_t)(lo - b) * kClipUnit, end < a.numel[t] ? end : a.numel[t]);
-    }
-    if (kBackwards) u1 = lo < u1 ? lo : u1, --t;
-    else u0 = hi > u0 ? hi : u0, ++t;
-  }
-}
-
-// Squares in float64: exact for float32 values, and without overflow or underflow. (One float64
-// multiply-add an element keeps up with the loads.)
-template <int DT>
-__device__ inline double sum_squares(const void* tensor, int64_t lo, int64_t hi) {
-  const auto* x = (const typename Row<DT>::Bits*)tensor;
-  double s[2] = {0.0, 0.0};
-  auto add = [&](const float (&v)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e & 1] = __builtin_fma((double)v[e], (double)v[e], s[e & 1]);
+  struct Part {
+    const void* src;
+    void* dst;
+    int64_t lo, hi;  // elements
+    bool f32, to_f32;
   };
-  const int64_t first = (int64_t)threadIdx.x * 8;
-  int64_t at = lo;
-  for (; at + kClipInFlight * kClipUnit <= hi; at += kClipInFlight * kClipUnit) {
-    typename Row<DT>::Chunk c[kClipInFlight];
-#pragma unroll
-    for (int u = 0; u < kClipInFlight; ++u) c[u] = Row<DT>::load(x + at + u * kClipUnit + first);
-#pragma unroll
-    for (int u = 0; u < kClipInFlight; ++u) {
-      float v[8];
-      Row<DT>::unpack(c[u], v);
-      add(v);
+  static constexpr uint64_t kAddress = (uint64_t{1} << 48) - 1, kF32 = uint64_t{1} << 61;
+  // Of global memory: without the address space the accesses would be flat ones.
+  __device__ static inline void* address(uint64_t word) {
+    return (void*)(__attribute__((address_space(1))) void*)(word & kAddress);
+  }
+  __device__ inline Part part(uint32_t unit) const {
+    uint32_t t = hint[unit >> hint_shift];
+    while (first[t + 1] <= unit) ++t;
+    const uint64_t s = src[t], d = kOut ? dst[t] : s;
+    const int64_t lo = (int64_t)(unit - first[t]) * kUnit;
+    const int64_t size = unit + 1 == first[t + 1] ? (int64_t)(s >> 48 & 0x1FFF) + 1 : kUnit;
+    return {address(s), address(d), lo, lo + size, (s & kF32) != 0, (d & kF32) != 0};
+  }
+
+  // The host's side: an empty table, a tensor of `numel` > 0 more (false: it is full), the end.
+  void begin() { n = 0, first[0] = 0; }
+  bool add(const void* tensor, int64_t numel, bool f32, void* out, bool to_f32) {
+    if (n == kN) return false;
+    const uint64_t last = (uint64_t)((numel - 1) % kUnit);
+    src[n] = reinterpret_cast<uint64_t>(tensor) | last << 48 | (f32 ? kF32 : 0);
+    if (kOut) dst[n] = reinterpret_cast<uint64_t>(out) | (to_f32 ? kF32 : 0);
+    first[n + 1] = first[n] + (uint32_t)((numel + kUnit - 1) / kUnit);
+    ++n;
+    return true;
+  }
+  void end() {
+    units = first[n], hint_shift = 0;
+    while ((units - 1) >> hint_shift >= (uint32_t)kHints) ++hint_shift;
+    int t = 0;
+    for (int i = 0; i < kHints; ++i) {
+      const uint64_t unit = (uint64_t)i << hint_shift;
+      while (t + 1 < n && first[t + 1] <= unit) ++t;
+      hint[i] = (uint32_t)t;
     }
   }
-  for (at += first; at < hi; at += kClipUnit) {
-    if (at + 8 <= hi) {
-      float v[8];
-      Row<DT>::unpack(Row<DT>::load(x + at), v);
-      add(v);
-    } else {
-      for (int64_t i = at; i < hi; ++i) {
-        const double v = (double)Row<DT>::get(x + i);
-        s[0] = __builtin_fma(v, v, s[0]);
+};
+
+using NormTable = ClipTable<304, 8192, false>;
+using ScaleTable = ClipTable<184, 2048, true>;
+
+// Pieces of a thread in a unit of the norm's table.
+template <int DT>
+constexpr int unit_pieces() { return (int)NormTable::kUnitSize / (kClipThreads * Piece<DT>::kSize); }
+
+// Squares in float64: exact for float32 values, and without overflow or underflow; one float64
+// multiply-add an element costs nothing beside the loads (2.1 GB 345 us, in float32 348).
+template <int DT>
+__device__ inline double sum_squares(const NormTable::Part& p) {
+  using P = Piece<DT>;
+  constexpr int kU = unit_pieces<DT>();
+  const auto* x = (const typename P::Bits*)p.src;
+  const int64_t first = p.lo + (int64_t)threadIdx.x * P::kSize;
+  constexpr int kStep = kClipThreads * P::kSize;
+  double s[2] = {0.0, 0.0};
+  auto add = [&](const P& c) {
+    float v[P::kSize];
+    c.unpack(v);
+#pragma unroll
+    for (int e = 0; e < P::kSize; ++e) s[e & 1] = __builtin_fma((double)v[e], (double)v[e], s[e & 1]);
+  };
+  if (p.hi - p.lo == NormTable::kUnitSize) {
+    P c[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) c[u] = P::load_once(x + first + u * kStep);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) add(c[u]);
+  } else {
+    for (int64_t at = first; at < p.hi; at += kStep) {
+      if (at + P::kSize <= p.hi) {
+        add(P::load_once(x + at));
+      } else {
+        for (int64_t i = at; i < p.hi; ++i) {
+          const double v = (double)Row<DT>::get(x + i);
+          s[0] = __builtin_fma(v, v, s[0]);
+        }
       }
     }
   }
@@ -118,91 +131,166 @@ __device__ inline double clip_block_sum(double s, double* sh) {
 __global__ void __launch_bounds__(kClipThreads, 8) clip_norm_kernel(NormTable a, double* partials) {
   __shared__ double sh[kClipWaves];
   double s = 0.0;
-  visit_span<false>(a, [&](int t, int64_t lo, int64_t hi) {
-    s += a.is_f32(t) ? sum_squares<TSC_DTYPE_F32>(a.src[t], lo, hi) : sum_squares<TSC_DTYPE_BF16>(a.src[t], lo, hi);
-  });
+  for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+    const auto p = a.part(unit);
+    s += p.f32 ? sum_squares<TSC_DTYPE_F32>(p) : sum_squares<TSC_DTYPE_BF16>(p);
+  }
   s = clip_block_sum(s, sh);
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
 }
 
+// The norm from its partial sums.
 __device__ inline float norm_of(const double* partials, int32_t n, double* sh) {
   double s = 0.0;
-  for (int32_t i = (int32_t)threadIdx.x; i < n; i += kClipThreads) s += partials[i];
+  for (int32_t i = (int32_t)threadIdx.x; i < n; i += kClipThreads * 8) {
+    double v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = i + u * kClipThreads < n ? partials[i + u * kClipThreads] : 0.0;
+    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  }
   return (float)sqrt(clip_block_sum(s, sh));
 }
 
-__global__ void __launch_bounds__(kClipThreads, 8) clip_join_kernel(const double* partials, int32_t n, float* norm) {
+__global__ void __launch_bounds__(kClipThreads) clip_join_kernel(const double* partials, int32_t n, float* norm) {
   __shared__ double sh[kClipWaves];
   const float v = norm_of(partials, n, sh);
   if (threadIdx.x == 0) *norm = v;
 }
 
-template <int DT, int OT>
-__device__ inline void scale_span(const void* tensor, void* out, int64_t lo, int64_t hi, float by) {
-  const auto* x = (const typename Row<DT>::Bits*)tensor;
-  auto* y = (typename Row<OT>::Bits*)out;
-  const int64_t first = (int64_t)threadIdx.x * 8;
-  // From the end: what the norm's pass has read last is still in the last-level cache.
-  int64_t end = lo + (hi - lo) / (kClipInFlight * kClipUnit) * (kClipInFlight * kClipUnit);
-  for (int64_t at = end + first; at < hi; at += kClipUnit) {
-    if (at + 8 <= hi) {
-      float v[8];
-      Row<DT>::unpack(Row<DT>::load(x + at), v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= by;
-      Row<OT>::store(y + at, v);
-    } else {
-      for (int64_t i = at; i < hi; ++i) Row<OT>::put(y + i, Row<DT>::get(x + i) * by);
-    }
-  }
-  while (end > lo) {
-    end -= kClipInFlight * kClipUnit;
-    typename Row<DT>::Chunk c[kClipInFlight];
-#pragma unroll
-    for (int u = 0; u < kClipInFlight; ++u) c[u] = Row<DT>::load(x + end + u * kClipUnit + first);
-#pragma unroll
-    for (int u = 0; u < kClipInFlight; ++u) {
-      float v[8];
-      Row<DT>::unpack(c[u], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= by;
-      Row<OT>::store(y + end + u * kClipUnit + first, v);
-    }
-  }
-}
-
-// The factor of a norm; values stay as they are below max_norm and where the norm is no number.
-__device__ inline float clip_factor(float norm, float max_norm) {
-  return norm > max_norm && norm < __builtin_inff() ? max_norm / norm : 1.0f;
-}
-
-// Scales by the norm of `n` partial sums, which workgroup 0 writes to `norm_out` (if not null), or
-// by *norm_in.
+// Where a scaling has its norm from: `n` partial sums, which workgroup 0 writes to `norm_out` (if
+// not null), or *norm_in.
 struct ClipNorm {
   const double* partials;
   int32_t n;
+  float max_norm;
   float* norm_out;
   const float* norm_in;
-  float max_norm;
-  int32_t in_place;  // nothing to do where the factor is 1
 };
 
-__global__ void __launch_bounds__(kClipThreads, 8) clip_scale_kernel(ScaleTable a, ClipNorm c) {
-  __shared__ double sh[kClipWaves];
+// The factor; values stay as they are up to max_norm and where the norm is no number.
+__device__ inline float clip_factor(const ClipNorm& c, double* sh) {
   const float norm = c.norm_in ? *c.norm_in : norm_of(c.partials, c.n, sh);
   if (c.norm_out && blockIdx.x == 0 && threadIdx.x == 0) *c.norm_out = norm;
-  const float by = clip_factor(norm, c.max_norm);
-  if (by == 1.0f && c.in_place) return;
-  visit_span<true>(a, [&](int t, int64_t lo, int64_t hi) {
-    const void* x = a.src[t];
-    void* y = a.dst[t];
-    if (a.is_f32(t))
-      a.to_f32(t) ? scale_span<TSC_DTYPE_F32, TSC_DTYPE_F32>(x, y, lo, hi, by)
-                  : scale_span<TSC_DTYPE_F32, TSC_DTYPE_BF16>(x, y, lo, hi, by);
-    else
-      a.to_f32(t) ? scale_span<TSC_DTYPE_BF16, TSC_DTYPE_F32>(x, y, lo, hi, by)
-                  : scale_span<TSC_DTYPE_BF16, TSC_DTYPE_BF16>(x, y, lo, hi, by);
-  });
+  return norm > c.max_norm && norm < __builtin_inff() ? c.max_norm / norm : 1.0f;
+}
+
+// In place: nothing to do where the factor is 1. A workgroup takes several units, as many as leave
+// a grid that is soon through when there is nothing to do (each wave of an empty one costs 50 ps:
+// a grid of one unit of 2048 elements each 76 us for 357 million elements).
+template <int DT>
+__device__ inline void scale_unit(const NormTable::Part& p, float by) {
+  using P = Piece<DT>;
+  constexpr int kU = unit_pieces<DT>();
+  auto* x = (typename P::Bits*)p.dst;
+  const int64_t first = p.lo + (int64_t)threadIdx.x * P::kSize;
+  constexpr int kStep = kClipThreads * P::kSize;
+  auto put = [&](const P& c, int64_t at) {
+    float v[P::kSize];
+    c.unpack(v);
+#pragma unroll
+    for (int e = 0; e < P::kSize; ++e) v[e] *= by;
+    P::store(x + at, v);
+  };
+  if (p.hi - p.lo == NormTable::kUnitSize) {
+    P c[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) c[u] = P::load_once(x + first + u * kStep);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) put(c[u], first + u * kStep);
+  } else {
+    for (int64_t at = first; at < p.hi; at += kStep) {
+      if (at + P::kSize <= p.hi) put(P::load_once(x + at), at);
+      else
+        for (int64_t i = at; i < p.hi; ++i) Row<DT>::put(x + i, Row<DT>::get(x + i) * by);
+    }
+  }
+}
+
+constexpr int64_t kInPlaceGroups = 16384;
+
+__global__ void __launch_bounds__(kClipThreads, 8) clip_in_place_kernel(NormTable a, ClipNorm c) {
+  __shared__ double sh[kClipWaves];
+  const float by = clip_factor(c, sh);
+  if (by == 1.0f) return;
+  for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+    const auto p = a.part(unit);
+    p.f32 ? scale_unit<TSC_DTYPE_F32>(p, by) : scale_unit<TSC_DTYPE_BF16>(p, by);
+  }
+}
+
+// Into other tensors: a unit per workgroup, 8 elements a thread, which is near what the memory does
+// fastest. 1.12 billion elements from bfloat16 to float32 (6.7 GB) take 1060 us, 6.3 TB/s; 4 elements
+// a thread 1440 (its load waits for the table's), 16 1075 to 1140, 32 1200; a contiguous span for
+// each of 1024 workgroups and 16-byte stores 32 bytes apart 1850.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_by2 __attribute__((aligned(2)));
+
+// kE elements of a thread: a piece, or half of one where the other side's piece has 4.
+template <int DT, int kE>
+__device__ inline void load_few(const typename Row<DT>::Bits* p, float (&v)[kE]) {
+  if constexpr (kE == Piece<DT>::kSize) {
+    Piece<DT>::load_once(p).unpack(v);
+  } else {
+    static_assert(DT == TSC_DTYPE_BF16 && kE == 4, "half a piece");
+    const u32x2 c = __builtin_nontemporal_load(reinterpret_cast<const u32x2_by2*>(p));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[2 * i] = __uint_as_float(c[i] << 16), v[2 * i + 1] = __uint_as_float(c[i] & 0xFFFF0000u);
+  }
+}
+template <int OT, int kE>
+__device__ inline void store_few(typename Row<OT>::Bits* p, const float (&v)[kE]) {
+  if constexpr (kE == Piece<OT>::kSize) {
+    Piece<OT>::store(p, v);
+  } else {
+    u32x2 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * i]) |
+             (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * i + 1]) << 16;
+    __builtin_nontemporal_store((u32x2_by2)r, reinterpret_cast<u32x2_by2*>(p));
+  }
+}
+
+// The values are asked for before the factor is, which comes from memory too.
+template <int DT, int OT, int kE, class Factor>
+__device__ inline void copy_unit(const ScaleTable::Part& p, Factor factor) {
+  constexpr int kU = ScaleTable::kUnitSize / (kClipThreads * kE), kStep = kClipThreads * kE;
+  const auto* x = (const typename Row<DT>::Bits*)p.src;
+  auto* y = (typename Row<OT>::Bits*)p.dst;
+  const int64_t at = p.lo + (int64_t)threadIdx.x * kE;
+  if (p.hi - p.lo == ScaleTable::kUnitSize) {
+    float v[kU][kE];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load_few<DT, kE>(x + at + u * kStep, v[u]);
+    const float by = factor();
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[u][e] *= by;
+      store_few<OT, kE>(y + at + u * kStep, v[u]);
+    }
+  } else {
+    const float by = factor();
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      for (int64_t i = at + u * kStep; i < at + u * kStep + kE && i < p.hi; ++i)
+        Row<OT>::put(y + i, Row<DT>::get(x + i) * by);
+  }
+}
+
+// kE 8: a table of bfloat16 tensors with bfloat16 results; 4: any.
+template <int kE>
+__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(ScaleTable a, ClipNorm c) {
+  constexpr int F = TSC_DTYPE_F32, B = TSC_DTYPE_BF16;
+  __shared__ double sh[kClipWaves];
+  float by = 0.0f;
+  for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+    const auto p = a.part(unit);
+    auto factor = [&] { return unit == blockIdx.x ? by = clip_factor(c, sh) : by; };
+    if constexpr (kE == 8) copy_unit<B, B, 8>(p, factor);
+    else if (p.f32) p.to_f32 ? copy_unit<F, F, 4>(p, factor) : copy_unit<F, B, 4>(p, factor);
+    else p.to_f32 ? copy_unit<B, F, 4>(p, factor) : copy_unit<B, B, 4>(p, factor);
+  }
 }
 
 }  // namespace tsc

@@ -15,8 +15,7 @@ namespace {
 
 constexpr int64_t kMaxTensors = int64_t{1} << 20;
 constexpr int64_t kMaxElements = int64_t{1} << 40;
-// Up to so many partial sums every workgroup of the scaling adds up by itself, which saves a launch.
-constexpr int64_t kJoinInline = 4 * tsc::kClipGroups;
+constexpr int64_t kJoinInline = int64_t{1} << 20;  // reads of partial sums
 
 int64_t size_of(int32_t dtype) { return dtype == TSC_DTYPE_F32 ? 4 : 2; }
 
@@ -27,8 +26,8 @@ int32_t check_list(const void* const* tensors, const int64_t* numels, const int3
   for (int64_t i = 0; i < count; ++i) {
     if (!dtype_ok(dtypes[i]) || numels[i] < 0) return TSC_ERR_INVALID_ARGUMENT;
     if (numels[i] >= kMaxElements || (all += numels[i]) >= kMaxElements) return TSC_ERR_UNSUPPORTED;
-    if (numels[i] > 0 && (!tensors[i] || !aligned(tensors[i], dtypes[i])))
-      return TSC_ERR_INVALID_ARGUMENT;
+    if (numels[i] > 0 && (!tensors[i] || !aligned(tensors[i], dtypes[i]))) return TSC_ERR_INVALID_ARGUMENT;
+    if (numels[i] > 0 && reinterpret_cast<uintptr_t>(tensors[i]) >> 48 != 0) return TSC_ERR_INVALID_ARGUMENT;
   }
   return TSC_OK;
 }
@@ -76,38 +75,32 @@ int32_t check_out(const Lists& l) {
   return TSC_OK;
 }
 
-// Tensors [from, ...) into an empty table, as many as fit; returns the index behind them. The
-// tensors' addresses and types are the caller's to add.
-template <class Table, class Add>
-int64_t fill(Table& t, const Lists& l, int64_t from, Add add) {
-  t.n = 0;
-  t.first[0] = 0;
+// Tensors from index `from` on into a table, as many as fit; returns the index behind them.
+template <class Table>
+int64_t fill(Table& t, const Lists& l, int64_t from) {
+  t.begin();
   int64_t i = from;
-  for (; i < l.count && t.n < Table::kSize; ++i) {
-    const int64_t units = ceil_div(l.numels[i], tsc::kClipUnit);
-    if (units == 0) continue;
-    t.src[t.n] = l.src[i];
-    t.numel[t.n] = l.numels[i];
-    if (l.dtypes[i] == TSC_DTYPE_F32) t.f32[t.n >> 5] |= 1u << (t.n & 31);
-    add(t.n, i);
-    t.first[t.n + 1] = t.first[t.n] + (uint32_t)units;
-    ++t.n;
-  }
+  for (; i < l.count; ++i)
+    if (l.numels[i] > 0 && !t.add(l.src[i], l.numels[i], l.dtypes[i] == TSC_DTYPE_F32,
+                                  reinterpret_cast<void*>(l.out_begin(i)), l.out_dtype(i) == TSC_DTYPE_F32))
+      break;
+  if (t.n > 0) t.end();
   return i;
 }
 
 template <class Table>
-unsigned groups(const Table& t) { return t.first[t.n] < (uint32_t)tsc::kClipGroups ? t.first[t.n] : (unsigned)tsc::kClipGroups; }
+int64_t groups(const Table& t, int64_t most) { return t.units < most ? t.units : most; }
 
 // Launches the sums; returns how many partial sums they leave.
 int64_t launch_norm(const Lists& l, double* partials, hipStream_t s) {
   int64_t n = 0;
   for (int64_t i = 0; i < l.count;) {
-    tsc::NormTable t{};
-    i = fill(t, l, i, [](int32_t, int64_t) {});
+    tsc::NormTable t;
+    i = fill(t, l, i);
     if (t.n == 0) break;
-    hipLaunchKernelGGL(tsc::clip_norm_kernel, dim3(groups(t)), dim3(tsc::kClipThreads), 0, s, t, partials + n);
-    n += groups(t);
+    const int64_t g = groups(t, tsc::kClipGroups);
+    hipLaunchKernelGGL(tsc::clip_norm_kernel, dim3((unsigned)g), dim3(tsc::kClipThreads), 0, s, t, partials + n);
+    n += g;
   }
   return n;
 }
@@ -116,26 +109,43 @@ void launch_join(const double* partials, int64_t n, float* norm, hipStream_t s) 
   hipLaunchKernelGGL(tsc::clip_join_kernel, dim3(1), dim3(tsc::kClipThreads), 0, s, partials, (int32_t)n, norm);
 }
 
-void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
-  c.in_place = 1;
+bool in_place(const Lists& l) {
   for (int64_t i = 0; i < l.count; ++i)
-    if (l.numels[i] > 0 && !l.own(i)) c.in_place = 0;
-  // Tables of up to kSize tensors, the last ones first: the norm's pass has read those last.
-  for (int64_t end = l.count; end > 0;) {
-    const int64_t from = end > tsc::ScaleTable::kSize ? end - tsc::ScaleTable::kSize : 0;
-    Lists part = l;
-    part.count = end;
-    tsc::ScaleTable t{};
-    fill(t, part, from, [&](int32_t k, int64_t i) {
-      t.dst[k] = reinterpret_cast<void*>(l.out_begin(i));
-      if (l.out_dtype(i) == TSC_DTYPE_F32) t.dst_f32[k >> 5] |= 1u << (k & 31);
-    });
-    if (t.n > 0) {
-      hipLaunchKernelGGL(tsc::clip_scale_kernel, dim3(groups(t)), dim3(tsc::kClipThreads), 0, s, t, c);
-      c.norm_out = nullptr;  // written once
+    if (l.numels[i] > 0 && !l.own(i)) return false;
+  return true;
+}
+
+void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
+  const bool own = in_place(l);
+  for (int64_t i = 0; i < l.count;) {
+    if (own) {
+      tsc::NormTable t;
+      i = fill(t, l, i);
+      if (t.n == 0) break;
+      hipLaunchKernelGGL(tsc::clip_in_place_kernel, dim3((unsigned)groups(t, tsc::kInPlaceGroups)),
+                         dim3(tsc::kClipThreads), 0, s, t, c);
+    } else {
+      tsc::ScaleTable t;
+      const int64_t from = i;
+      i = fill(t, l, i);
+      if (t.n == 0) break;
+      bool narrow = true;
+      for (int64_t k = from; k < i; ++k)
+        narrow = narrow && (l.numels[k] == 0 || (l.dtypes[k] == TSC_DTYPE_BF16 && l.out_dtype(k) == TSC_DTYPE_BF16));
+      const dim3 grid((unsigned)groups(t, kMaxRows));
+      if (narrow) hipLaunchKernelGGL(tsc::clip_scale_kernel<8>, grid, dim3(tsc::kClipThreads), 0, s, t, c);
+      else hipLaunchKernelGGL(tsc::clip_scale_kernel<4>, grid, dim3(tsc::kClipThreads), 0, s, t, c);
     }
-    end = from;
+    c.norm_out = nullptr;  // written once
   }
+}
+
+// Whether every workgroup of the scaling may add up the partial sums by itself, which saves a
+// launch: few of either.
+bool joins_inline(const Lists& l, int64_t partials) {
+  int64_t units = 0;
+  for (int64_t i = 0; i < l.count; ++i) units += ceil_div(l.numels[i], tsc::ScaleTable::kUnitSize);
+  return partials > 0 && partials * units <= kJoinInline;
 }
 
 int32_t check_norm(float* norm, int64_t count, const void* workspace, size_t have) {
@@ -176,11 +186,11 @@ int32_t tsc_clip_grad_norm(const void* const* tensors, const int64_t* numels, co
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   double* partials = static_cast<double*>(workspace);
   const int64_t n = launch_norm(l, partials, s);
-  if (n == 0 || n > kJoinInline) {
-    launch_join(partials, n, norm, s);
-    launch_scale(l, {nullptr, 0, nullptr, norm, max_norm, 0}, s);
+  if (joins_inline(l, n)) {
+    launch_scale(l, {partials, (int32_t)n, max_norm, norm, nullptr}, s);
   } else {
-    launch_scale(l, {partials, (int32_t)n, norm, nullptr, max_norm, 0}, s);
+    launch_join(partials, n, norm, s);
+    launch_scale(l, {nullptr, 0, max_norm, nullptr, norm}, s);
   }
   return launched();
 } catch (const std::bad_alloc&) {
@@ -195,7 +205,7 @@ int32_t tsc_clip_grads(const void* const* tensors, const int64_t* numels, const 
   const Lists l{tensors, numels, dtypes, count, out, out_dtypes};
   if (const int32_t e = check_out(l)) return e;
   (void)hipGetLastError();
-  launch_scale(l, {nullptr, 0, nullptr, norm, max_norm, 0}, reinterpret_cast<hipStream_t>(stream));
+  launch_scale(l, {nullptr, 0, max_norm, nullptr, norm}, reinterpret_cast<hipStream_t>(stream));
   return launched();
 } catch (const std::bad_alloc&) {
   return TSC_ERR_INVALID_ARGUMENT;

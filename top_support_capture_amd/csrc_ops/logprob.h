@@ -42,6 +42,8 @@ struct LogprobArgs {
   void* grad;                  // [N, V], contiguous
   int32_t segments;
   int64_t seg_len;
+  int32_t held;  // pieces a thread of the fused kernel keeps in LDS
+  int32_t once;  // the logits are not read again soon, and are more than the caches hold
   __device__ inline float T(int64_t n) const { return temperature ? temperature[n] : 1.0f; }
 };
 
@@ -49,33 +51,32 @@ struct LogprobArgs {
 constexpr float kLeastExponent = -200.0f;
 
 // A thread's running state: sums of up to 32 terms in float32, all else in float64. `at` is the
-// first chunk (kTop only) that reached the maximum, -1 before the first one.
+// first piece (kTop only) that reached the maximum, -1 before the first one.
 template <bool kEnt, bool kTop>
 struct LogprobState {
   float m = -__builtin_inff();
   int32_t at = -1;
   double s = 0.0, a = 0.0;
-  // U chunks of 8 elements, the first chunk's index and the distance from one to the next.
-  template <int U>
-  __device__ inline void add(const float (&x)[U * 8], float c, int32_t chunk, int32_t step) {
+  // kU pieces of kE elements, the first piece's index and the distance from one to the next.
+  template <int kU, int kE>
+  __device__ inline void add(const float (&x)[kU][kE], float c, int32_t piece, int32_t step) {
     float b = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float* v = x + u * 8;
-      const float most = __builtin_fmaxf(
-          __builtin_fmaxf(__builtin_fmaxf(v[0], v[1]), __builtin_fmaxf(v[2], v[3])),
-          __builtin_fmaxf(__builtin_fmaxf(v[4], v[5]), __builtin_fmaxf(v[6], v[7])));
+    for (int u = 0; u < kU; ++u) {
+      float most = x[u][0];
+#pragma unroll
+      for (int e = 1; e < kE; ++e) most = __builtin_fmaxf(most, x[u][e]);
       if constexpr (kTop) {
-        if (most > b) at = chunk + u * step;
+        if (most > b) at = piece + u * step;
       }
       b = __builtin_fmaxf(b, most);
     }
-    if constexpr (kTop) at = at < 0 ? chunk : at;
+    if constexpr (kTop) at = at < 0 ? piece : at;
     const float base = b == -__builtin_inff() ? 0.0f : b;
     float t4[4] = {}, a4[4] = {};
 #pragma unroll
-    for (int i = 0; i < U * 8; ++i) {
-      const float t = (x[i] - base) * c, e = __builtin_amdgcn_exp2f(t);
+    for (int i = 0; i < kU * kE; ++i) {
+      const float t = (x[i / kE][i % kE] - base) * c, e = __builtin_amdgcn_exp2f(t);
       t4[i & 3] += e;
       if constexpr (kEnt) a4[i & 3] = __builtin_fmaf(e, __builtin_fmaxf(t, kLeastExponent), a4[i & 3]);
     }
@@ -110,36 +111,65 @@ __device__ inline LogprobPart block_part(LogprobState<kEnt, kTop> st, float c, L
   if (lane == 0) sh.m[w] = st.m, sh.s[w] = ws, sh.a[w] = wa;
   lds_barrier();
   LogprobState<kEnt, kTop> v;
-  const uint32_t from = lane & (kW - 1);
-  v.m = sh.m[from], v.s = sh.s[from], v.a = sh.a[from];
-  static_assert(kW == 16, "one partial for each lane of a row of 16");
+  const uint32_t from = lane & 15u;
+  static_assert(kW <= 16, "a partial for each lane of a row of 16");
+  if (from < kW) v.m = sh.m[from], v.s = sh.s[from], v.a = sh.a[from];
   v.rescale(row16_reduce(v.m, [](float p, float q) { return __builtin_fmaxf(p, q); }), c);
   return {v.m, row16_reduce(v.s, SumOp()), kEnt ? row16_reduce(v.a, SumOp()) : 0.0};
 }
 
-// A thread's state of row[lo, hi), lo a multiple of 8, in a workgroup of kTopThreads threads.
-template <int DT, bool kEnt, bool kTop>
+// The first pieces of a row, kept in LDS from one pass over it to the next: `pieces` a thread.
+template <int kThr>
+struct HeldPieces {
+  u32x4* at;
+  int32_t pieces;
+  __device__ inline void put(int64_t k, const u32x4& v) const {
+    if (k < pieces) at[k * kThr + threadIdx.x] = v;  // uniform
+  }
+};
+struct NothingHeld {
+  __device__ inline void put(int64_t, const u32x4&) const {}
+};
+
+// A thread's state of row[lo, hi), lo a multiple of 8, in a workgroup of kThr threads. (32 float32
+// elements in flight per thread instead of 16 spill where alternatives are kept, and gain nothing.)
+template <int DT, int kThr, bool kEnt, bool kTop, class Held = NothingHeld>
 __device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
-                                                        float c) {
-  constexpr int kU = 4;  // chunks in flight per thread
-  constexpr int64_t kStep = kTopRound;
+                                                        float c, bool once = false, Held held = Held()) {
+  constexpr int kE = Piece<DT>::kSize, kU = 4;  // pieces in flight per thread
+  constexpr int64_t kStep = kThr * kE;
   LogprobState<kEnt, kTop> st;
-  const int64_t first = (int64_t)threadIdx.x * 8;
-  int64_t base = lo;
-  for (; base + kU * kStep <= hi; base += kU * kStep) {
-    typename Row<DT>::Chunk v[kU];
+  int64_t at = lo + (int64_t)threadIdx.x * kE;
+  for (int64_t base = lo; base < hi; base += kU * kStep, at += kU * kStep) {
+    Piece<DT> v[kU];
+    float x[kU][kE];
+    const bool last = base + kU * kStep > hi;  // uniform
+    if (!last && once) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) v[u] = Row<DT>::load(row + base + u * kStep + first);
-    float f[kU * 8];
+      for (int u = 0; u < kU; ++u) v[u] = Piece<DT>::load_once(row + at + u * kStep);
+    } else if (!last) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) Row<DT>::unpack(v[u], reinterpret_cast<float(&)[8]>(f[u * 8]));
-    st.template add<kU>(f, c, (int32_t)((base + first) >> 3), (int32_t)(kStep >> 3));
+      for (int u = 0; u < kU; ++u) v[u] = Piece<DT>::load(row + at + u * kStep);
+    } else {  // all at once too; -inf behind the end
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        v[u] = Piece<DT>::lowest();
+        if (at + u * kStep + kE <= hi) v[u] = Piece<DT>::load(row + at + u * kStep);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      v[u].unpack(x[u]);
+      held.put((base - lo) / kStep + u, v[u].v);
+    }
+    if (last) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (at + u * kStep < hi && at + u * kStep + kE > hi) load_part<DT>(row, at + u * kStep, hi, x[u]);
+    }
+    st.add(x, c, (int32_t)(at / kE), (int32_t)(kStep / kE));
   }
-  for (int64_t at = base + first; at < hi; at += kStep) {
-    float x[8];
-    load8<DT>(row, at, hi, x);
-    st.template add<1>(x, c, (int32_t)(at >> 3), 0);
-  }
+  if (lo + (int64_t)threadIdx.x * kE >= hi) st.at = -1;  // nothing of the row
   return st;
 }
 
@@ -161,75 +191,73 @@ __device__ inline int32_t logprob_early_status(const LogprobArgs& a, int64_t n) 
   return t < -1 || t >= a.V || !temperature_ok(a.T(n)) ? TSC_ROW_INVALID_PARAM : TSC_ROW_OK;
 }
 
-// Row n's outputs but the alternatives: thread 0 writes, every thread gets the row. `x` is the
-// token's logit.
+__device__ inline int32_t logprob_status(int32_t early, const LogprobPart& p) {
+  if (early != TSC_ROW_OK) return early;
+  if (!(p.s < __builtin_inf()) || !(p.m < __builtin_inff())) return TSC_ROW_NONFINITE;
+  return p.m == -__builtin_inff() ? TSC_ROW_NO_SUPPORT : TSC_ROW_OK;
+}
+
+// Row n's outputs: `x` is the token's logit (thread 0), top the a.top first keys of a row that is OK.
+// The first waves write, each thread one alternative; every thread gets the row.
 __device__ inline LogprobRow logprob_finish(const LogprobArgs& a, int64_t n, int32_t status, const LogprobPart& p,
-                                            float x) {
-  if (status == TSC_ROW_OK) {
-    if (!(p.s < __builtin_inf()) || !(p.m < __builtin_inff())) status = TSC_ROW_NONFINITE;
-    else if (p.m == -__builtin_inff()) status = TSC_ROW_NO_SUPPORT;
-  }
+                                            float x, const uint64_t* top) {
   const bool ok = status == TSC_ROW_OK;
+  const int32_t tid = (int32_t)threadIdx.x, last_wave = a.top > 0 ? (a.top - 1) / kWaveSize : 0;
   const double M = ok ? p.a / p.s * 0.69314718055994530942 : 0.0;
-  if (threadIdx.x == 0) {
-    const bool padding = a.tokens[n] == -1;
-    const double ln_s = ok ? log(p.s) : 0.0;
-    const float none = padding ? 0.0f : __builtin_nanf("");
-    a.logprobs[n] = ok ? (float)(((double)x - (double)p.m) / (double)a.T(n) - ln_s) : none;
-    if (a.entropy) a.entropy[n] = ok ? (float)(ln_s - M) : none;
-    a.row_status[n] = (int8_t)status;
-    if (a.stats) {
-      float* st = a.stats + n * 4;
-      st[0] = ok ? p.m : 0.0f, st[1] = ok ? (float)p.s : 1.0f;
-      st[2] = a.entropy ? (float)M : __builtin_nanf("");  // asked for without the entropy: shows
-      st[3] = ok ? 1.0f : 0.0f;
+  if (tid / kWaveSize <= last_wave) {
+    const double ln_s = ok ? log(p.s) : 0.0, inv_T = 1.0 / (double)a.T(n);
+    if (tid < a.top) {
+      const uint64_t key = ok ? top[tid] : 0;
+      a.top_ids[n * a.top + tid] = ok ? key_id(key) : -1;
+      a.top_logprobs[n * a.top + tid] =
+          ok ? (float)(((double)key_value(key) - (double)p.m) * inv_T - ln_s) : __builtin_nanf("");
+    }
+    if (tid == 0) {
+      const float none = a.tokens[n] == -1 ? 0.0f : __builtin_nanf("");
+      a.logprobs[n] = ok ? (float)(((double)x - (double)p.m) * inv_T - ln_s) : none;
+      if (a.entropy) a.entropy[n] = ok ? (float)(ln_s - M) : none;
+      a.row_status[n] = (int8_t)status;
+      if (a.stats) {
+        float* st = a.stats + n * 4;
+        st[0] = ok ? p.m : 0.0f, st[1] = ok ? (float)p.s : 1.0f;
+        st[2] = a.entropy ? (float)M : __builtin_nanf("");  // asked for without the entropy: shows
+        st[3] = ok ? 1.0f : 0.0f;
+      }
     }
   }
   return {p.m, (float)p.s, (float)M, ok};
 }
 
-// The alternatives of a row that is not OK.
-__device__ inline void logprob_no_top(const LogprobArgs& a, int64_t n) {
-  for (int32_t i = (int32_t)threadIdx.x; i < a.top; i += kTopThreads)
-    a.top_ids[n * a.top + i] = -1, a.top_logprobs[n * a.top + i] = __builtin_nanf("");
-}
-
-// Place r of row n's alternatives.
-__device__ inline void logprob_put_top(const LogprobArgs& a, int64_t n, const LogprobPart& p, int r, uint64_t key) {
-  a.top_ids[n * a.top + r] = key_id(key);
-  a.top_logprobs[n * a.top + r] =
-      (float)(((double)key_value(key) - (double)p.m) / (double)a.T(n) - log(p.s));
-}
-
 // A row per workgroup, read once.
-template <int DT, bool kEnt, bool kTop>
-__global__ void __launch_bounds__(kTopThreads, 8) logprob_kernel(LogprobArgs a) {
+template <int DT, int kThr, bool kEnt, bool kTop>
+__global__ void __launch_bounds__(kThr, 8) logprob_kernel(LogprobArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
-  __shared__ LogprobShared<kTopWaves> sh;
+  __shared__ LogprobShared<kThr / kWaveSize> sh;
   __shared__ TopShared top;
   const int64_t n = blockIdx.x;
-  const int32_t status = logprob_early_status(a, n);
+  const int32_t early = logprob_early_status(a, n);
   LogprobPart p{-__builtin_inff(), 0.0, 0.0};
   const auto* row = (const typename Row<DT>::Bits*)a.logits + n * a.ld;
   float x = 0.0f;
   uint64_t key = 0;
-  if (status == TSC_ROW_OK) {
+  if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get(row + a.tokens[n]);
     const float c = plain_scale(a.T(n));
-    const auto st = logprob_pass<DT, kEnt, kTop>(row, 0, a.V, c);
+    const auto st = logprob_pass<DT, kThr, kEnt, kTop>(row, 0, a.V, c, a.once != 0);
     if constexpr (kTop) key = state_key(st);
-    p = block_part<kTopWaves>(st, c, sh);
+    p = block_part<kThr / kWaveSize>(st, c, sh);
   }
-  const LogprobRow r = logprob_finish(a, n, status, p, x);
+  const int32_t status = logprob_status(early, p);
+  const uint64_t* first = nullptr;
   if constexpr (kTop) {
-    if (!r.ok) {
-      logprob_no_top(a, n);
-      return;
+    static_assert(kThr == kTopThreads, "the selection's workgroup");
+    if (status == TSC_ROW_OK) {
+      const TopLists lists(dyn_top);
+      top_collect<DT>(row, 0, a.V, key, a.top, lists, top);
+      first = top_sort(lists.cand, a.top, top);
     }
-    const TopLists lists(dyn_top);
-    top_collect<DT>(row, 0, a.V, key, a.top, lists, top);
-    top_emit(lists.cand, a.top, top, [&](int at, uint64_t k) { logprob_put_top(a, n, p, at, k); });
   }
+  logprob_finish(a, n, status, p, x, first);
 }
 
 // Few rows: a slice of a row per workgroup, then the rows from their slices.
@@ -239,17 +267,18 @@ __global__ void __launch_bounds__(kTopThreads, 8) logprob_slice_kernel(LogprobAr
   __shared__ LogprobShared<kTopWaves> sh;
   __shared__ TopShared top;
   const int64_t item = blockIdx.x, n = item / a.slices, sl = item - n * a.slices;
-  if (logprob_early_status(a, n) != TSC_ROW_OK) return;
   const int64_t lo = sl * a.slice_len, hi = lo + a.slice_len < a.V ? lo + a.slice_len : a.V;
   const auto* row = (const typename Row<DT>::Bits*)a.logits + n * a.ld;
   const float c = plain_scale(a.T(n));
-  const auto st = logprob_pass<DT, kEnt, kTop>(row, lo, hi, c);
+  const auto st = logprob_pass<DT, kTopThreads, kEnt, kTop>(row, lo, hi, c);
+  if (logprob_early_status(a, n) != TSC_ROW_OK) return;  // not looked at earlier: the row is on its way by now
   const LogprobPart p = block_part<kTopWaves>(st, c, sh);
   if (threadIdx.x == 0) a.parts[item] = p;
   if constexpr (kTop) {
     const TopLists lists(dyn_top);
     top_collect<DT>(row, lo, hi, state_key(st), a.top, lists, top);
-    top_emit(lists.cand, a.top, top, [&](int at, uint64_t k) { a.keys[item * a.top + at] = k; });
+    const uint64_t* first = top_sort(lists.cand, a.top, top);
+    if ((int32_t)threadIdx.x < a.top) a.keys[item * a.top + threadIdx.x] = first[threadIdx.x];
   }
 }
 
@@ -258,10 +287,10 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
   extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
   __shared__ TopShared top;
   const int64_t n = blockIdx.x;
-  const int32_t status = logprob_early_status(a, n), lane = (int32_t)threadIdx.x & (kWaveSize - 1);
+  const int32_t early = logprob_early_status(a, n), lane = (int32_t)threadIdx.x & (kWaveSize - 1);
   LogprobPart p{-__builtin_inff(), 0.0, 0.0};
   float x = 0.0f;
-  if (status == TSC_ROW_OK) {
+  if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get((const typename Row<DT>::Bits*)a.logits + n * a.ld + a.tokens[n]);
     const float c = plain_scale(a.T(n));
     LogprobState<kEnt, kTop> st;
@@ -272,16 +301,16 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
     st.rescale(wave_max(st.m), c);
     p = {st.m, wave_reduce(st.s, SumOp()), kEnt ? wave_reduce(st.a, SumOp()) : 0.0};
   }
-  const LogprobRow r = logprob_finish(a, n, status, p, x);
+  const int32_t status = logprob_status(early, p);
+  const uint64_t* first = nullptr;
   if constexpr (kTop) {
-    if (!r.ok) {
-      logprob_no_top(a, n);
-      return;
+    if (status == TSC_ROW_OK) {
+      const TopLists lists(dyn_top);
+      top_collect_keys(a.keys + n * a.slices * a.top, a.slices, a.top, lists, top);
+      first = top_sort(lists.cand, a.top, top);
     }
-    const TopLists lists(dyn_top);
-    top_collect_keys(a.keys + n * a.slices * a.top, a.slices * a.top, a.top, lists, top);
-    top_emit(lists.cand, a.top, top, [&](int at, uint64_t k) { logprob_put_top(a, n, p, at, k); });
   }
+  logprob_finish(a, n, status, p, x, first);
 }
 
 // ---- the gradient ----------------------------------------------------------------------------------
@@ -297,64 +326,67 @@ __device__ inline LogprobCoef logprob_coef(const LogprobRow& r, float T, float t
   return {r.m, plain_scale(T), (b == 0.0f ? -total : __builtin_fmaf(b, r.M, -total)) * g, -b * 0.69314718055994531f * g};
 }
 
-__device__ inline void logprob_grad8(float (&x)[8], const LogprobCoef& k) {
+template <int kE>
+__device__ inline void logprob_grad_of(float (&x)[kE], const LogprobCoef& k) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < kE; ++e) {
     const float t = __builtin_fmaxf((x[e] - k.m) * k.c, kLeastExponent);
     x[e] = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(k.beta, t, k.alpha);
   }
 }
 
-// Writes the gradient of row[lo, hi). at_chunk(at, x) adds what stands beside the stream to the
-// chunk from `at` on.
-template <int DT, int kThr, class AtChunk>
+// Writes the gradient of row[lo, hi), kU pieces in flight per thread. beside(at, x) adds what stands
+// beside the stream to the piece from `at` on.
+template <int DT, int kThr, int kU, class Beside>
 __device__ inline void logprob_grad_pass(const typename Row<DT>::Bits* row, typename Row<DT>::Bits* out, int64_t lo,
-                                         int64_t hi, const LogprobCoef& k, AtChunk at_chunk) {
-  constexpr int kU = DT == TSC_DTYPE_BF16 ? 4 : 2;  // chunks in flight per thread
-  constexpr int64_t kStep = (int64_t)kThr * 8;
-  const int64_t first = (int64_t)threadIdx.x * 8;
+                                         int64_t hi, const LogprobCoef& k, Beside beside) {
+  constexpr int kE = Piece<DT>::kSize;
+  constexpr int64_t kStep = kThr * kE;
+  int64_t at = lo + (int64_t)threadIdx.x * kE;
   int64_t base = lo;
-  for (; base + kU * kStep <= hi; base += kU * kStep) {
-    typename Row<DT>::Chunk v[kU];
+  for (; base + kU * kStep <= hi; base += kU * kStep, at += kU * kStep) {
+    Piece<DT> v[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) v[u] = Row<DT>::load_once(row + base + u * kStep + first);
+    for (int u = 0; u < kU; ++u) v[u] = Piece<DT>::load_once(row + at + u * kStep);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      float x[8];
-      Row<DT>::unpack(v[u], x);
-      logprob_grad8(x, k);
-      at_chunk(base + u * kStep + first, x);
-      Row<DT>::store(out + base + u * kStep + first, x);
+      float x[kE];
+      v[u].unpack(x);
+      logprob_grad_of(x, k);
+      beside(at + u * kStep, x);
+      Piece<DT>::store(out + at + u * kStep, x);
     }
   }
-  for (int64_t at = base + first; at < hi; at += kStep) {
-    float x[8];
-    load8<DT>(row, at, hi, x);
-    logprob_grad8(x, k);
-    at_chunk(at, x);
-    store8<DT>(out, at, hi, x);
+  for (; at < hi; at += kStep) {
+    float x[kE];
+    load_piece<DT>(row, at, hi, x);
+    logprob_grad_of(x, k);
+    beside(at, x);
+    store_piece<DT>(out, at, hi, x);
   }
 }
 
-// x[i] += v, i in [0, 8): without an index into registers.
-__device__ inline void add_at(float (&x)[8], uint32_t i, float v) {
+// x[i] += v: without an index into registers.
+template <int kE>
+__device__ inline void add_at(float (&x)[kE], uint32_t i, float v) {
 #pragma unroll
-  for (uint32_t e = 0; e < 8; ++e) x[e] += e == i ? v : 0.0f;
+  for (uint32_t e = 0; e < kE; ++e) x[e] += e == i ? v : 0.0f;
 }
 
-constexpr int kLogprobGradThreads = 256;
+constexpr int kLogprobGradThreads = 256, kLogprobGradPieces = 4;  // in flight per thread
+constexpr int64_t kLogprobGradSegment = 8192;  // elements, or more to bound the grid
 
-// A segment of a row per workgroup. With alternatives (kTop), a bit for each chunk of the segment
-// that holds one says where the list is looked through.
+// A segment of a row per workgroup. With alternatives (kTop), a bit for each 8 elements of the segment
+// that hold one says where the list is looked through.
 template <int DT, bool kTop>
 __global__ void __launch_bounds__(kLogprobGradThreads, 8) logprob_grad_kernel(LogprobArgs a) {
-  constexpr int kThr = kLogprobGradThreads;
+  constexpr int kThr = kLogprobGradThreads, kE = Piece<DT>::kSize;
   using B = typename Row<DT>::Bits;
   __shared__ uint32_t bits[kTop ? kMaxSegment / 8 / 32 : 1];
   __shared__ int32_t ids[kTop ? kTopMost : 1];
   __shared__ float ups[kTop ? kTopMost : 1];
-  const int64_t n = blockIdx.x / a.segments;
-  const int64_t lo = (blockIdx.x - n * a.segments) * a.seg_len;
+  const int64_t item = blockIdx.x, n = item / a.segments;
+  const int64_t lo = (item - n * a.segments) * a.seg_len;
   const int64_t hi = lo + a.seg_len < a.V ? lo + a.seg_len : a.V;
   B* out = (B*)a.grad + n * a.V;
   const float* st = a.stats + n * 4;
@@ -382,46 +414,60 @@ __global__ void __launch_bounds__(kLogprobGradThreads, 8) logprob_grad_kernel(Lo
   }
   const LogprobCoef k = logprob_coef(r, T, total, a.grad_entropy ? a.grad_entropy[n] : 0.0f);
   const float hit = up / T;
-  logprob_grad_pass<DT, kThr>(row, out, lo, hi, k, [&](int64_t at, float(&x)[8]) {
-    if ((uint64_t)(token - at) < 8u) add_at(x, (uint32_t)(token - at), hit);
+  logprob_grad_pass<DT, kThr, kLogprobGradPieces>(row, out, lo, hi, k, [&](int64_t at, float(&x)[kE]) {
+    if ((uint64_t)(token - at) < (unsigned)kE) add_at(x, (uint32_t)(token - at), hit);
     if constexpr (kTop) {
       const uint32_t chunk = (uint32_t)(at - lo) >> 3;
       if ((bits[chunk >> 5] >> (chunk & 31)) & 1u) {
         for (int j = 0; j < a.top; ++j)
-          if ((uint64_t)(ids[j] - at) < 8u) add_at(x, (uint32_t)(ids[j] - at), ups[j] / T);
+          if ((uint64_t)(ids[j] - at) < (unsigned)kE) add_at(x, (uint32_t)(ids[j] - at), ups[j] / T);
       }
     }
   });
 }
 
-// Values and gradient, a row per workgroup: the second reading of the row comes from the last-level
-// cache while the rows in flight fit there.
-template <int DT, bool kEnt>
-__global__ void __launch_bounds__(kTopThreads, 8) logprob_fused_kernel(LogprobArgs a) {
+// Values and gradient, a row per workgroup: the second reading of the row comes from LDS as far as
+// that goes, and from the last-level cache while the rows in flight fit there.
+template <int DT, int kThr, bool kEnt>
+__global__ void __launch_bounds__(kThr, 8) logprob_fused_kernel(LogprobArgs a) {
   using B = typename Row<DT>::Bits;
-  __shared__ LogprobShared<kTopWaves> sh;
+  extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
+  __shared__ LogprobShared<kThr / kWaveSize> sh;
+  constexpr int kE = Piece<DT>::kSize;
+  const HeldPieces<kThr> held{reinterpret_cast<u32x4*>(dyn_top), a.held};
   const int64_t n = blockIdx.x;
-  const int32_t status = logprob_early_status(a, n);
+  const int32_t early = logprob_early_status(a, n);
   LogprobPart p{-__builtin_inff(), 0.0, 0.0};
   const B* row = (const B*)a.logits + n * a.ld;
   B* out = (B*)a.grad + n * a.V;
   float x = 0.0f;
   const float T = a.T(n), c = plain_scale(T);
-  if (status == TSC_ROW_OK) {
+  if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get(row + a.tokens[n]);
-    p = block_part<kTopWaves>(logprob_pass<DT, kEnt, false>(row, 0, a.V, c), c, sh);
+    p = block_part<kThr / kWaveSize>(logprob_pass<DT, kThr, kEnt, false>(row, 0, a.V, c, false, held), c, sh);
   }
-  const LogprobRow r = logprob_finish(a, n, status, p, x);
+  const LogprobRow r = logprob_finish(a, n, logprob_status(early, p), p, x, nullptr);
   if (!r.ok) {
-    fill_zero<DT, kTopThreads>(out, 0, a.V);
+    fill_zero<DT, kThr>(out, 0, a.V);
     return;
   }
   const float up = a.grad_logprobs[n], hit = up / T;
   const int64_t token = a.tokens[n];
   const LogprobCoef k = logprob_coef(r, T, up, a.grad_entropy ? a.grad_entropy[n] : 0.0f);
-  logprob_grad_pass<DT, kTopThreads>(row, out, 0, a.V, k, [&](int64_t at, float(&v)[8]) {
-    if ((uint64_t)(token - at) < 8u) add_at(v, (uint32_t)(token - at), hit);
-  });
+  auto beside = [&](int64_t at, float(&v)[kE]) {
+    if ((uint64_t)(token - at) < (unsigned)kE) add_at(v, (uint32_t)(token - at), hit);
+  };
+  // Whole steps of the workgroup that every thread holds.
+  int64_t lo = 0;
+  for (int32_t i = 0; i < a.held && lo + kThr * kE <= a.V; ++i, lo += kThr * kE) {
+    float v[kE];
+    Piece<DT>{held.at[i * kThr + threadIdx.x]}.unpack(v);
+    const int64_t at = lo + (int64_t)threadIdx.x * kE;
+    logprob_grad_of(v, k);
+    beside(at, v);
+    Piece<DT>::store(out + at, v);
+  }
+  logprob_grad_pass<DT, kThr, 4>(row, out, lo, a.V, k, beside);
 }
 
 }  // namespace tsc

@@ -11,17 +11,30 @@ namespace {
 
 static_assert(TSC_MAX_TOP == tsc::kTopMost, "the selection's lists hold that many");
 
-// Whole rows for a workgroup each when there are rows enough, or short ones; slices otherwise.
+// Whole rows for a workgroup each when there are rows enough, or short ones; slices otherwise, as
+// many as the chip holds at once (two workgroups on each CU), of 8192 elements at least, and whole
+// steps of a workgroup for either type.
 Cut pass_cut(int64_t N, int64_t V) {
-  return N >= 128 || V <= 65536 ? Cut{1, V} : cut_rows(N, V, tsc::kTopRound, 4 * tsc::kTopRound, 512);
+  if (N >= 128 || V <= 65536) return {1, V};
+  const int64_t most = ceil_div(V, 8192) < tsc::kMaxSlices ? ceil_div(V, 8192) : tsc::kMaxSlices;
+  const int64_t n = 512 / (N > 0 ? N : 1) < most ? 512 / (N > 0 ? N : 1) : most;
+  const int64_t len = ceil_div(ceil_div(V, n), 4096) * 4096;
+  return {(int32_t)ceil_div(V, len), len};
 }
 
-// The gradient: segments of 16384 elements, longer ones only to bound the grid.
 Cut segment_cut(int64_t N, int64_t V) {
-  int64_t len = 16384;
+  int64_t len = tsc::kLogprobGradSegment;
   while (len < tsc::kMaxSegment && N * ceil_div(V, len) > (int64_t{1} << 22)) len *= 2;
   return {(int32_t)ceil_div(V, len), len};
 }
+
+constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
+
+// With this many rows a smaller workgroup reads one, so that the ends of some overlap the loads of
+// others. (With entropies, bf16: 4096 rows of 2000 take 18 us against 54, of 32000 55 against 68, 1024
+// rows of 151936 61 against 64; but 256 rows of those 28 against 20.)
+constexpr int64_t kManyRows = 1024;
+constexpr int kSmall = 256;
 
 int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld) {
   if (!dtype_ok(dtype) || N < 0 || V < 1 || V > kMaxVocab || ld < V) return TSC_ERR_INVALID_ARGUMENT;
@@ -61,8 +74,13 @@ hipError_t launch_top(Kernel kernel, const tsc::LogprobArgs& a, int64_t groups, 
 template <int DT, bool kEnt, bool kTop>
 hipError_t launch_pass(const tsc::LogprobArgs& a, hipStream_t s) {
   static std::atomic<uint64_t> whole{0}, slice{0}, join{0};
-  if (a.slices == 1)
-    return launch_top(&tsc::logprob_kernel<DT, kEnt, kTop>, a, a.N, tsc::kTopThreads, kTop, whole, s);
+  if (a.slices == 1) {
+    if constexpr (!kTop) {
+      if (a.N >= kManyRows)
+        return launch_top(&tsc::logprob_kernel<DT, kSmall, kEnt, false>, a, a.N, kSmall, false, whole, s);
+    }
+    return launch_top(&tsc::logprob_kernel<DT, tsc::kTopThreads, kEnt, kTop>, a, a.N, tsc::kTopThreads, kTop, whole, s);
+  }
   const hipError_t err =
       launch_top(&tsc::logprob_slice_kernel<DT, kEnt, kTop>, a, a.N * a.slices, tsc::kTopThreads, kTop, slice, s);
   if (err != hipSuccess) return err;
@@ -100,21 +118,29 @@ hipError_t launch_grad(tsc::LogprobArgs& a, int32_t dtype, hipStream_t s) {
 // short; one launch instead of two or three.
 bool fused(int64_t N, int64_t V) { return N >= 128 || V <= 65536; }
 
-// The fused kernel's second reading of a row comes from the last-level cache (256 MB), if the rows
-// of all resident workgroups fit there: past kCached bytes of rows one workgroup is kept to a CU,
-// by asking for more than half of its LDS.
-constexpr int64_t kCached = 180 << 20;
-constexpr size_t kAlone = 84 * 1024;
+// A second reading of a row comes from the last-level cache if the rows of all resident workgroups
+// fit there, beside the gradients on their way out.
+constexpr int64_t kCached = kCacheBytes * 7 / 10;
+
+// LDS that holds the first pieces of a workgroup's row for the second reading, as much as leaves room
+// for two large workgroups, or eight small ones, on a CU.
+template <int DT, int kThr, bool kEnt>
+hipError_t launch_fused(tsc::LogprobArgs a, hipStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  constexpr size_t kHeld = (kThr == kSmall ? 16 : 64) << 10;
+  const auto kernel = &tsc::logprob_fused_kernel<DT, kThr, kEnt>;
+  const hipError_t err = allow_lds(kernel, kHeld, allowed);
+  if (err != hipSuccess) return err;
+  a.held = (int32_t)(kHeld / (kThr * 16));
+  hipLaunchKernelGGL(kernel, dim3((unsigned)a.N), dim3(kThr), kHeld, s, a);
+  return hipGetLastError();
+}
 
 template <int DT, bool kEnt>
 hipError_t launch_fused(const tsc::LogprobArgs& a, hipStream_t s) {
-  static std::atomic<uint64_t> allowed{0};
-  const auto kernel = &tsc::logprob_fused_kernel<DT, kEnt>;
-  const int64_t rows = (a.N < 512 ? a.N : 512) * a.V * (DT == TSC_DTYPE_F32 ? 4 : 2);
-  const hipError_t err = allow_lds(kernel, kAlone, allowed);
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)a.N), dim3(tsc::kTopThreads), rows > kCached ? kAlone : 0, s, a);
-  return hipGetLastError();
+  const int64_t rows = 2048 * a.V * (DT == TSC_DTYPE_F32 ? 4 : 2);  // of 8 workgroups on each CU
+  return a.N >= kManyRows && rows <= kCached ? launch_fused<DT, kSmall, kEnt>(a, s)
+                                             : launch_fused<DT, tsc::kTopThreads, kEnt>(a, s);
 }
 
 hipError_t launch_fused(const tsc::LogprobArgs& a, int32_t dtype, bool entropy, hipStream_t s) {
@@ -147,6 +173,9 @@ int32_t tsc_token_logprobs(const void* logits, int32_t dtype, int64_t N, int64_t
   a.logprobs = logprobs, a.entropy = entropy, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
   a.row_status = row_status, a.stats = stats;
   set_parts(a, static_cast<char*>(workspace));
+  // Values alone: logits past the caches' size are read nontemporally (4096 rows of 151936 bfloat16 201
+  // us against 212). Not where the backward pass reads them again (85 us against 110 behind that).
+  a.once = stats == nullptr && N * V * (dtype == TSC_DTYPE_F32 ? 4 : 2) > kCacheBytes;
   (void)hipGetLastError();  // start from a clean error state so a launch error is ours
   return launch_pass(a, dtype, entropy != nullptr, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? TSC_OK
                                                                                                        : TSC_ERR_HIP;

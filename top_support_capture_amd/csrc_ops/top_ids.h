@@ -1,14 +1,14 @@
 // The n first elements of a row in (value desc, id asc) order, n small, beside a pass over the row
 // that is made anyway.
 //
-// While a thread reads its chunks of 8 elements it keeps the maximum and the first chunk that holds
-// it: its key, (value, earlier chunk first). Any element among the row's n first lies in a thread
-// whose key is among the n best keys: each better key stands for an element that precedes every
-// element of the thread. So a bound below the n-th best key leaves few threads, whose chunks are
-// read once more and compared with the bound; what reaches it is ranked.
+// While a thread reads its pieces it keeps the maximum and the first piece that holds it: its key,
+// (value, earlier piece first). Any element among the row's n first lies in a thread whose key is
+// among the n best keys: each better key stands for an element that precedes every element of the
+// thread. So a bound below the n-th best key leaves few threads, whose pieces are read once more and
+// compared with the bound; what reaches it is ranked.
 #pragma once
 
-#include "row_stats.h"
+#include "piece.h"
 
 namespace tsc {
 
@@ -21,21 +21,21 @@ __device__ inline float from_order_bits(uint32_t o) {
   return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// Keys in 64 bits, greater ones first; 0 stands for none. Of an element, or of a chunk.
+// Keys in 64 bits, greater ones first; 0 stands for none. Of an element, or of a piece.
 __device__ inline uint64_t top_key(float x, uint32_t id) { return (uint64_t)order_bits(x) << 32 | (uint32_t)~id; }
 __device__ inline float key_value(uint64_t k) { return from_order_bits((uint32_t)(k >> 32)); }
 __device__ inline int32_t key_id(uint64_t k) { return (int32_t)~(uint32_t)k; }
-// The least key that an element of the chunks up to this one's can have at its value.
-__device__ inline uint64_t chunk_bound(uint64_t k) {
-  return k == 0 ? 0 : (k >> 32 << 32) | (uint32_t)~(~(uint32_t)k * 8u + 7u);
+// The least key that an element of the pieces up to this one's can have at its value.
+template <int kPiece>
+__device__ inline uint64_t piece_bound(uint64_t k) {
+  return k == 0 ? 0 : (k >> 32 << 32) | (uint32_t)~(~(uint32_t)k * kPiece + (kPiece - 1));
 }
 
 constexpr int kTopThreads = 1024;
 constexpr int kTopWaves = kTopThreads / kWaveSize;
 constexpr int kTopMost = 128;          // n
 constexpr int kTopFew = 512;           // candidates that are ranked by counting
-constexpr int kTopRound = kTopThreads * 8;
-constexpr int kTopCap = kTopFew + kTopRound;
+constexpr int kTopCap = kTopFew + kTopThreads * 8;  // those, and a round of pieces of 8
 constexpr int kTopPerWave = kTopMost / kTopWaves + 1;
 
 // A workgroup's LDS for the selection: kTopLds bytes of dynamic LDS, and this.
@@ -53,26 +53,58 @@ struct TopLists {
 };
 constexpr size_t kTopLds = kTopCap * 8 + kTopThreads * 2;
 
+// How many of list[0, c) are greater than `mine`, which 16 neighbouring lanes ask for together: each
+// takes every 16th. (One thread to a key, reading the list by itself, took the largest part of the
+// selection: every read is waited for.)
+__device__ inline int count_above(const uint64_t* list, int c, uint64_t mine) {
+  int above = 0;
+#pragma unroll 4
+  for (int i = (int)threadIdx.x & 15; i < c; i += 16) above += list[i] > mine;
+  above += dpp_mov<dpp::kQuadSwap1>(above, above);
+  above += dpp_mov<dpp::kQuadSwap2>(above, above);
+  above += dpp_mov<dpp::kRowRor4>(above, above);
+  return above + dpp_mov<dpp::kRowRor8>(above, above);
+}
+constexpr int kTopGroups = kTopThreads / 16;
+
+// The n-th greatest of list[0, c), 0 if there are fewer (keys other than 0 are distinct). Needs
+// sh.bound == 0 and a barrier before, and a barrier behind it.
+__device__ inline void top_nth(const uint64_t* list, int c, int n, TopShared& sh) {
+  for (int g = 0; g < c; g += kTopGroups) {
+    const int i = g + ((int)threadIdx.x >> 4);
+    const uint64_t mine = i < c ? list[i] : 0;
+    if (count_above(list, c, mine) == n - 1 && mine != 0) sh.bound = mine;
+  }
+}
+
+// The greatest of the wave's keys: by the values, and by the rest only where values tie.
+__device__ inline uint64_t wave_best(uint64_t key) {
+  const uint32_t hi = (uint32_t)(key >> 32), most = wave_reduce(hi, MaxOp());
+  const uint64_t at = __ballot(hi == most);
+  if ((at & (at - 1)) == 0) return read_lane(key, __builtin_ctzll(at));
+  return (uint64_t)most << 32 | wave_reduce(hi == most ? (uint32_t)key : 0u, MaxOp());
+}
+
 // A key that at least n of the threads' keys reach, near the n-th best: the n-th best among each
-// wave's best few; 0 if those are fewer than n.
-__device__ inline uint64_t top_bound(uint64_t key, int n, TopShared& sh) {
+// wave's best few; 0 if those are fewer than n. Where only the first threads have a key (`some`),
+// they are dealt out to all waves first.
+__device__ inline uint64_t top_bound(uint64_t key, int n, bool some, const TopLists& lists, TopShared& sh) {
   const uint32_t tid = threadIdx.x, w = tid / kWaveSize;
   const int per = (n + kTopWaves - 1) / kTopWaves + (n > 1 ? 1 : 0);  // at most kTopPerWave
   lds_barrier();  // sh may still be read by an earlier call
+  if (some) {
+    lists.cand[tid] = key;
+    lds_barrier();
+    key = lists.cand[(tid & 15) * kWaveSize + (tid >> 4)];
+  }
   for (int i = 0; i < per; ++i) {
-    const uint64_t best = wave_reduce(key, MaxOp());
+    const uint64_t best = wave_best(key);
     if (key == best) key = 0;
     if ((tid & (kWaveSize - 1)) == 0) sh.wave[w * per + i] = best;
   }
   if (tid == 0) sh.bound = 0;
   lds_barrier();
-  const int all = kTopWaves * per;
-  if ((int)tid < all) {
-    const uint64_t mine = sh.wave[tid];
-    int above = 0;
-    for (int i = 0; i < all; ++i) above += sh.wave[i] > mine;
-    if (above == n - 1 && mine != 0) sh.bound = mine;
-  }
+  top_nth(sh.wave, kTopWaves * per, n, sh);
   lds_barrier();
   return sh.bound;
 }
@@ -120,68 +152,117 @@ __device__ inline uint64_t top_narrow(uint64_t* cand, int c, int n, TopShared& s
   return prefix;
 }
 
-// emit(r, key) for the n first of the sh.count candidates, r their place; one thread each. Fewer
-// than n candidates: emit(r, 0) for the places behind them.
-template <class Emit>
-__device__ inline void top_emit(uint64_t* cand, int n, TopShared& sh, Emit emit) {
+// The n first of the sh.count candidates in order, and 0 behind them if they are fewer: sh.wave[0, n),
+// once all threads are through.
+__device__ inline const uint64_t* top_sort(uint64_t* cand, int n, TopShared& sh) {
+  static_assert(kTopWaves * kTopPerWave >= kTopMost, "room for the result");
   lds_barrier();
   if ((int)sh.count > kTopFew) top_narrow(cand, (int)sh.count, n, sh);
   const int c = (int)sh.count, tid = (int)threadIdx.x;
-  if (tid < c) {
-    const uint64_t mine = cand[tid];
-    int above = 0;
-    for (int i = 0; i < c; ++i) above += cand[i] > mine;
-    if (above < n) emit(above, mine);
+  for (int g = 0; g < c; g += kTopGroups) {
+    const int i = g + (tid >> 4);
+    const uint64_t mine = i < c ? cand[i] : 0;
+    const int above = count_above(cand, c, mine);
+    if ((tid & 15) == 0 && i < c && above < n) sh.wave[above] = mine;
   }
-  if (tid >= c && tid < n) emit(tid, uint64_t{0});
+  if (tid >= c && tid < n) sh.wave[tid] = 0;
+  lds_barrier();
+  return sh.wave;
 }
 
 // The candidates among row[lo, hi), lo a multiple of 8, from the threads' keys (0 of a thread that
 // has read nothing), into lists.cand and sh.count: all of the n first (as many as there are) and
-// few others. Thread t has read the chunks from lo + 8 t on in steps of kTopRound elements.
+// few others. Thread t has read the pieces from lo + t pieces on in steps of kTopThreads.
 template <int DT>
 __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi, uint64_t key, int n,
                                    const TopLists& lists, TopShared& sh) {
+  constexpr int kSize = Piece<DT>::kSize, kStep = kTopThreads * kSize;
   const uint32_t tid = threadIdx.x;
-  const uint64_t threads_bound = top_bound(key, n, sh);
-  uint64_t bound = chunk_bound(threads_bound);
+  const uint64_t threads_bound = top_bound(key, n, hi - lo < kStep, lists, sh);
+  uint64_t bound = piece_bound<kSize>(threads_bound);
   if (tid == 0) sh.count = 0, sh.threads = 0;
   lds_barrier();
   if (key != 0 && key >= threads_bound) lists.thread[atomicAdd(&sh.threads, 1u)] = (uint16_t)tid;
   lds_barrier();
-  const uint32_t steps = (uint32_t)((hi - lo + kTopRound - 1) / kTopRound);
-  const uint32_t items = sh.threads * steps;  // at most 2^10 * 2^18
-  for (uint32_t j0 = 0; j0 < items; j0 += kTopThreads) {
-    const uint32_t j = j0 + tid;
-    if (j < items) {
-      const uint32_t i = j / steps;
-      const int64_t at = lo + (int64_t)(j - i * steps) * kTopRound + (int64_t)lists.thread[i] * 8;
-      if (at < hi) {
-        float x[8];
-        load8<DT>(row, at, hi, x);
+  const uint32_t steps = (uint32_t)((hi - lo + kStep - 1) / kStep);
+  const uint32_t items = sh.threads * steps;  // pieces to read: at most 2^10 * 2^19
+  // Item j is piece j % steps of the thread j / steps of the list; from round to round by addition.
+  const uint32_t di = kTopThreads / steps, dr = kTopThreads - di * steps;
+  uint32_t i = tid / steps, r = tid - i * steps;
+  // kB rounds of pieces from item j0 on, all in flight together; what does not fit is counted.
+  auto rounds = [&](uint32_t j0, auto blocks) {
+    constexpr int kB = decltype(blocks)::value;
+    float x[kB][kSize];
+    int64_t at[kB];
+    const uint32_t wave_first = j0 + (tid & ~(uint32_t)(kWaveSize - 1));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t k = top_key(x[e], (uint32_t)(at + e));
-          if (k >= bound && at + e < hi) lists.cand[atomicAdd(&sh.count, 1u)] = k;
+    for (int b = 0; b < kB; ++b) {
+      at[b] = hi;
+      if (wave_first + b * kTopThreads < items) {  // the same for the wave
+        if (j0 + b * kTopThreads + tid < items) at[b] = lo + (int64_t)r * kStep + (int64_t)lists.thread[i] * kSize;
+        Piece<DT> v = Piece<DT>::lowest();
+        if (at[b] + kSize <= hi) v = Piece<DT>::load(row + at[b]);
+        v.unpack(x[b]);
+      }
+      i += di, r += dr;
+      if (r >= steps) r -= steps, ++i;
+    }
+    const float least = bound == 0 ? -__builtin_inff() : key_value(bound);
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      if (wave_first + b * kTopThreads >= items) continue;
+      if (at[b] < hi && at[b] + kSize > hi) load_part<DT>(row, at[b], hi, x[b]);
+      uint32_t reach = 0;  // elements that reach the bound's value: few
+#pragma unroll
+      for (int e = 0; e < kSize; ++e) reach |= x[b][e] >= least && at[b] + e < hi ? 1u << e : 0u;
+      for (; reach != 0; reach &= reach - 1) {
+        const int e = __builtin_ctz(reach);
+        float v = x[b][0];
+#pragma unroll
+        for (int f = 1; f < kSize; ++f) v = e == f ? x[b][f] : v;
+        const uint64_t k = top_key(v, (uint32_t)(at[b] + e));
+        if (k >= bound) {
+          const uint32_t to = atomicAdd(&sh.count, 1u);
+          if (to < (uint32_t)kTopCap) lists.cand[to] = k;
         }
       }
     }
     lds_barrier();
     const uint32_t have = sh.count;
-    lds_barrier();  // every thread has the same count: the next round adds to it
-    // Room for another round. Rows in an order that piles their first elements up get here.
+    lds_barrier();  // every thread has the same count: the next rounds add to it
+    return have;
+  };
+  constexpr uint32_t kBatch = 2;
+  bool fits = true;
+  for (uint32_t j0 = 0; j0 < items && fits; j0 += kBatch * kTopThreads) {
+    const uint32_t have = rounds(j0, std::integral_constant<int, kBatch>());
+    fits = have <= (uint32_t)kTopCap;
+    if (fits && j0 + kBatch * kTopThreads < items && have > (uint32_t)kTopFew)
+      bound = top_narrow(lists.cand, (int)have, n, sh);
+  }
+  if (fits) return;
+  // Rows in an order that piles their first elements up: from the start, a round that always fits
+  // at a time.
+  if (tid == 0) sh.count = 0;
+  lds_barrier();
+  i = tid / steps, r = tid - i * steps;
+  for (uint32_t j0 = 0; j0 < items; j0 += kTopThreads) {
+    const uint32_t have = rounds(j0, std::integral_constant<int, 1>());
     if (j0 + kTopThreads < items && have > (uint32_t)kTopFew) bound = top_narrow(lists.cand, (int)have, n, sh);
   }
 }
 
-// The candidates among `count` keys (0: none) in memory: as above.
-__device__ inline void top_collect_keys(const uint64_t* keys, int count, int n, const TopLists& lists, TopShared& sh) {
-  const int tid = (int)threadIdx.x;
-  uint64_t key = 0;
-  for (int i = tid; i < count; i += kTopThreads) key = key > keys[i] ? key : keys[i];
-  const uint64_t bound = top_bound(key, n, sh);
-  if (tid == 0) sh.count = 0;
+// The candidates among the keys of `slices` (at most kMaxSlices) slices in memory, n of each, in
+// order: as above. The n-th best among each slice's first few bounds them.
+__device__ inline void top_collect_keys(const uint64_t* keys, int slices, int n, const TopLists& lists, TopShared& sh) {
+  const int tid = (int)threadIdx.x, count = slices * n;
+  const int some = (n + slices - 1) / slices + 2, per = some < n ? some : n;  // slices * per < n + 3 slices
+  for (int i = tid; i < slices * per; i += kTopThreads) lists.cand[i] = keys[i / per * n + i % per];
+  if (tid == 0) sh.bound = 0, sh.count = 0;
   lds_barrier();
+  top_nth(lists.cand, slices * per, n, sh);
+  lds_barrier();
+  const uint64_t bound = sh.bound;
   for (int i = tid; i < count; i += kTopThreads)  // at most kTopCap
     if (keys[i] != 0 && keys[i] >= bound) lists.cand[atomicAdd(&sh.count, 1u)] = keys[i];
   lds_barrier();

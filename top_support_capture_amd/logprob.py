@@ -7,6 +7,7 @@ pass runs on the stream that the forward ran on, allocates the gradient, and syn
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import NamedTuple, Optional
 
 import torch
@@ -37,6 +38,17 @@ class TokenLogprobsGradOutput(NamedTuple):
     row_status: torch.Tensor         # int8 [N]
 
 
+# Sizes are asked for once.
+@lru_cache(maxsize=256)
+def _workspace(N: int, V: int, top: int) -> int:
+    return library().tsc_token_logprobs_workspace(N, V, top)
+
+
+@lru_cache(maxsize=256)
+def _grad_workspace(N: int, V: int) -> int:
+    return library().tsc_token_logprobs_grad_workspace(N, V)
+
+
 def _args(logits, tokens, temperature):
     dt, N, V, ld, dev = _rows(logits)
     _check(tokens, "tokens", torch.int32, N, dev)
@@ -53,7 +65,7 @@ def _forward(logits, tokens, temperature, top, return_entropy, with_stats, strea
     args, N, V, dev = _args(logits, tokens, temperature)
     if not 0 <= top <= min(V, MAX_TOP):
         raise ValueError(f"top must be in 0..{min(V, MAX_TOP)}")
-    nbytes = lib.tsc_token_logprobs_workspace(N, V, top)
+    nbytes = _workspace(N, V, top)
 
     def go(s):
         f32 = dict(dtype=torch.float32, device=dev)
@@ -159,7 +171,7 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, grad_logprob
     _check(grad_logprobs, "grad_logprobs", torch.float32, N, dev)
     if grad_entropy is not None:
         _check(grad_entropy, "grad_entropy", torch.float32, N, dev)
-    nbytes = lib.tsc_token_logprobs_grad_workspace(N, V)
+    nbytes = _grad_workspace(N, V)
 
     def go(s):
         f32 = dict(dtype=torch.float32, device=dev)
