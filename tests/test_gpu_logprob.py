@@ -157,6 +157,42 @@ def test_against_the_oracle(N, V, dtype, top, entropy, pad, base):
     check_grad(x, dtype, T, tokens, rows, c, one.grad_logits)
 
 
+@pytest.mark.parametrize("N,V,dtype,top,entropy,pad", [
+    (1030, 2003, "bf16", 5, True, 1), (1024, 33000, "bf16", 20, False, 0), (1100, 300, "f32", 128, True, 0),
+    (1030, 131073, "bf16", 3, True, 1),    # more than the last-level cache holds
+    (1200, 90001, "f32", 0, True, 0), (1024, 20000, "f32", 0, False, 3),
+])
+def test_many_rows(N, V, dtype, top, entropy, pad):
+    # Rows enough for the smaller workgroups; some of them are compared.
+    log(f"case logprobs of many rows N={N} V={V} {dtype} top={top} entropy={entropy} pad={pad}")
+    g = torch.Generator(DEV).manual_seed(V)
+    buf = torch.randn(N, V + pad, device=DEV, generator=g).mul_(3).to(DT[dtype])
+    xt = buf[:, :V]
+    rng = np.random.default_rng(V)
+    tokens = rng.integers(0, V, N).astype(np.int32)
+    tokens[5] = -1
+    T = rng.uniform(0.5, 2, N).astype(np.float32)
+    tk, tt = tensor(tokens, torch.int32), tensor(T, torch.float32)
+    some = np.r_[0, 5, rng.permutation(N)[: 16 if V > 50000 else 60], N - 1]
+    at = torch.from_numpy(some).to(DEV)
+    x = xt[at].double().cpu().numpy()
+    cut = lambda out: out._replace(**{k: v[at] for k, v in out._asdict().items() if v is not None})
+    c = Case(rng, N, top, entropy)
+    few = Case(rng, 1, top, entropy)
+    few.a, few.b, few.u = (None if v is None else v[some] for v in (c.a, c.b, c.u))
+    out = tsc.token_logprobs(xt, tk, tt, top=top, return_entropy=entropy)
+    rows = check_values(x, T[some], tokens[some], top, cut(out), entropy)
+    leaf = xt.detach().requires_grad_()
+    again = tsc.token_logprobs(leaf, tk, tt, top=top, return_entropy=entropy)
+    assert all(a is None and b is None or torch.equal(a.nan_to_num(7), b.detach().nan_to_num(7)) for a, b in zip(out, again))
+    check_grad(x, dtype, T[some], tokens[some], rows, few, backward(leaf, again, c)[at])
+    few.u = None
+    one = tsc.token_logprobs_grad(xt, tk, tensor(c.a, torch.float32), tt,
+                                  grad_entropy=tensor(c.b, torch.float32) if entropy else None)
+    check_values(x, T[some], tokens[some], 0, cut(one), entropy)
+    check_grad(x, dtype, T[some], tokens[some], rows, few, one.grad_logits[at])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [600, 70000])
 def test_edges(dtype, V):
@@ -221,7 +257,8 @@ def arranged(V, order, rng):
 
 
 @pytest.mark.parametrize("order", ["ascending", "descending", "one thread", "one wave", "tied chunks"])
-@pytest.mark.parametrize("V,dtype,N", [(151936, "bf16", 1), (151936, "f32", 130), (30000, "bf16", 3), (200000, "f32", 2)])
+@pytest.mark.parametrize("V,dtype,N", [(151936, "bf16", 1), (151936, "f32", 130), (30000, "bf16", 3), (200000, "f32", 2),
+                                       (30000, "f32", 1100), (151936, "bf16", 128), (151936, "bf16", 1024)])
 def test_alternatives_wherever_they_lie(order, V, dtype, N):
     log(f"case alternatives {order} V={V} {dtype} N={N}")
     rng = np.random.default_rng(V)

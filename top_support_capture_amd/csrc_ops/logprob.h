@@ -13,6 +13,8 @@
 
 namespace tsc {
 
+constexpr int kTopThreads = 1024, kTopWaves = kTopThreads / kWaveSize;
+
 // State of a row or a part of it: the maximum, the sum of the numerators e = 2^t, t = (x - m) c,
 // and (kEnt) the sum of e t.
 struct LogprobPart {
@@ -43,7 +45,6 @@ struct LogprobArgs {
   int32_t segments;
   int64_t seg_len;
   int32_t held;  // pieces a thread of the fused kernel keeps in LDS
-  int32_t once;  // the logits are not read again soon, and are more than the caches hold
   __device__ inline float T(int64_t n) const { return temperature ? temperature[n] : 1.0f; }
 };
 
@@ -133,9 +134,9 @@ struct NothingHeld {
 
 // A thread's state of row[lo, hi), lo a multiple of 8, in a workgroup of kThr threads. (32 float32
 // elements in flight per thread instead of 16 spill where alternatives are kept, and gain nothing.)
-template <int DT, int kThr, bool kEnt, bool kTop, class Held = NothingHeld>
+template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce = false, class Held = NothingHeld>
 __device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
-                                                        float c, bool once = false, Held held = Held()) {
+                                                        float c, Held held = Held()) {
   constexpr int kE = Piece<DT>::kSize, kU = 4;  // pieces in flight per thread
   constexpr int64_t kStep = kThr * kE;
   LogprobState<kEnt, kTop> st;
@@ -144,12 +145,10 @@ __device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::
     Piece<DT> v[kU];
     float x[kU][kE];
     const bool last = base + kU * kStep > hi;  // uniform
-    if (!last && once) {
+    if (!last) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] = Piece<DT>::load_once(row + at + u * kStep);
-    } else if (!last) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] = Piece<DT>::load(row + at + u * kStep);
+      for (int u = 0; u < kU; ++u)
+        v[u] = kOnce ? Piece<DT>::load_once(row + at + u * kStep) : Piece<DT>::load(row + at + u * kStep);
     } else {  // all at once too; -inf behind the end
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -228,12 +227,12 @@ __device__ inline LogprobRow logprob_finish(const LogprobArgs& a, int64_t n, int
   return {p.m, (float)p.s, (float)M, ok};
 }
 
-// A row per workgroup, read once.
-template <int DT, int kThr, bool kEnt, bool kTop>
+// A row per workgroup, read once. kOnce: nontemporally.
+template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce>
 __global__ void __launch_bounds__(kThr, 8) logprob_kernel(LogprobArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
   __shared__ LogprobShared<kThr / kWaveSize> sh;
-  __shared__ TopShared top;
+  __shared__ TopShared<kThr> top;
   const int64_t n = blockIdx.x;
   const int32_t early = logprob_early_status(a, n);
   LogprobPart p{-__builtin_inff(), 0.0, 0.0};
@@ -243,16 +242,15 @@ __global__ void __launch_bounds__(kThr, 8) logprob_kernel(LogprobArgs a) {
   if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get(row + a.tokens[n]);
     const float c = plain_scale(a.T(n));
-    const auto st = logprob_pass<DT, kThr, kEnt, kTop>(row, 0, a.V, c, a.once != 0);
+    const auto st = logprob_pass<DT, kThr, kEnt, kTop, kOnce>(row, 0, a.V, c);
     if constexpr (kTop) key = state_key(st);
     p = block_part<kThr / kWaveSize>(st, c, sh);
   }
   const int32_t status = logprob_status(early, p);
   const uint64_t* first = nullptr;
   if constexpr (kTop) {
-    static_assert(kThr == kTopThreads, "the selection's workgroup");
     if (status == TSC_ROW_OK) {
-      const TopLists lists(dyn_top);
+      const TopLists<kThr> lists(dyn_top);
       top_collect<DT>(row, 0, a.V, key, a.top, lists, top);
       first = top_sort(lists.cand, a.top, top);
     }
@@ -265,7 +263,7 @@ template <int DT, bool kEnt, bool kTop>
 __global__ void __launch_bounds__(kTopThreads, 8) logprob_slice_kernel(LogprobArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
   __shared__ LogprobShared<kTopWaves> sh;
-  __shared__ TopShared top;
+  __shared__ TopShared<kTopThreads> top;
   const int64_t item = blockIdx.x, n = item / a.slices, sl = item - n * a.slices;
   const int64_t lo = sl * a.slice_len, hi = lo + a.slice_len < a.V ? lo + a.slice_len : a.V;
   const auto* row = (const typename Row<DT>::Bits*)a.logits + n * a.ld;
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(kTopThreads, 8) logprob_slice_kernel(LogprobAr
   const LogprobPart p = block_part<kTopWaves>(st, c, sh);
   if (threadIdx.x == 0) a.parts[item] = p;
   if constexpr (kTop) {
-    const TopLists lists(dyn_top);
+    const TopLists<kTopThreads> lists(dyn_top);
     top_collect<DT>(row, lo, hi, state_key(st), a.top, lists, top);
     const uint64_t* first = top_sort(lists.cand, a.top, top);
     if ((int32_t)threadIdx.x < a.top) a.keys[item * a.top + threadIdx.x] = first[threadIdx.x];
@@ -285,7 +283,7 @@ __global__ void __launch_bounds__(kTopThreads, 8) logprob_slice_kernel(LogprobAr
 template <int DT, bool kEnt, bool kTop>
 __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_kernel(LogprobArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
-  __shared__ TopShared top;
+  __shared__ TopShared<kTopThreads> top;
   const int64_t n = blockIdx.x;
   const int32_t early = logprob_early_status(a, n), lane = (int32_t)threadIdx.x & (kWaveSize - 1);
   LogprobPart p{-__builtin_inff(), 0.0, 0.0};
@@ -305,7 +303,7 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
   const uint64_t* first = nullptr;
   if constexpr (kTop) {
     if (status == TSC_ROW_OK) {
-      const TopLists lists(dyn_top);
+      const TopLists<kTopThreads> lists(dyn_top);
       top_collect_keys(a.keys + n * a.slices * a.top, a.slices, a.top, lists, top);
       first = top_sort(lists.cand, a.top, top);
     }
@@ -444,7 +442,7 @@ __global__ void __launch_bounds__(kThr, 8) logprob_fused_kernel(LogprobArgs a) {
   const float T = a.T(n), c = plain_scale(T);
   if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get(row + a.tokens[n]);
-    p = block_part<kThr / kWaveSize>(logprob_pass<DT, kThr, kEnt, false>(row, 0, a.V, c, false, held), c, sh);
+    p = block_part<kThr / kWaveSize>(logprob_pass<DT, kThr, kEnt, false>(row, 0, a.V, c, held), c, sh);
   }
   const LogprobRow r = logprob_finish(a, n, logprob_status(early, p), p, x, nullptr);
   if (!r.ok) {

@@ -32,9 +32,11 @@ constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
 
 // With this many rows a smaller workgroup reads one, so that the ends of some overlap the loads of
 // others. (With entropies, bf16: 4096 rows of 2000 take 18 us against 54, of 32000 55 against 68, 1024
-// rows of 151936 61 against 64; but 256 rows of those 28 against 20.)
+// rows of 151936 61 against 64; but 256 rows of those 28 against 20. With 5 alternatives 512 threads:
+// 4096 rows of 32000 73 us against 97, of 2000 44 against 81; with 20, of 151936 261 against 271 and, with
+// 256 threads, 287.)
 constexpr int64_t kManyRows = 1024;
-constexpr int kSmall = 256;
+constexpr int kSmall = 256, kSmallTop = 512;
 
 int32_t check_rows(const void* logits, int32_t dtype, int64_t N, int64_t V, int64_t ld) {
   if (!dtype_ok(dtype) || N < 0 || V < 1 || V > kMaxVocab || ld < V) return TSC_ERR_INVALID_ARGUMENT;
@@ -60,32 +62,46 @@ void set_parts(tsc::LogprobArgs& a, char* ws) {
   a.keys = reinterpret_cast<uint64_t*>(ws + parts_bytes(a.N, cut));
 }
 
-template <class Kernel>
-hipError_t launch_top(Kernel kernel, const tsc::LogprobArgs& a, int64_t groups, unsigned threads, bool top,
-                      std::atomic<uint64_t>& allowed, hipStream_t s) {
+// A kernel with the LDS of a selection by kThr threads, if it makes one.
+template <int kThr, class Kernel>
+hipError_t launch_top(Kernel kernel, const tsc::LogprobArgs& a, int64_t groups, bool top, std::atomic<uint64_t>& allowed,
+                      hipStream_t s) {
+  const size_t bytes = top ? tsc::TopLists<kThr>::kBytes : 0;
   if (top) {
-    const hipError_t err = allow_lds(kernel, tsc::kTopLds, allowed);
+    const hipError_t err = allow_lds(kernel, bytes, allowed);
     if (err != hipSuccess) return err;
   }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), top ? tsc::kTopLds : 0, s, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThr), bytes, s, a);
   return hipGetLastError();
+}
+
+// Values alone: logits past the last-level cache's size are read nontemporally (4096 rows of 151936
+// bfloat16, with the first alternative, 201 us against 212). Not where the backward pass reads them
+// again (83 us against 110 behind that).
+bool read_once(const tsc::LogprobArgs& a, int64_t size) {
+  return a.stats == nullptr && a.N * a.V * size > kCacheBytes;
+}
+
+template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce>
+hipError_t launch_rows(const tsc::LogprobArgs& a, hipStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  return launch_top<kThr>(&tsc::logprob_kernel<DT, kThr, kEnt, kTop, kOnce>, a, a.N, kTop, allowed, s);
 }
 
 template <int DT, bool kEnt, bool kTop>
 hipError_t launch_pass(const tsc::LogprobArgs& a, hipStream_t s) {
-  static std::atomic<uint64_t> whole{0}, slice{0}, join{0};
+  constexpr int kLarge = tsc::kTopThreads, kMany = kTop ? kSmallTop : kSmall;
   if (a.slices == 1) {
-    if constexpr (!kTop) {
-      if (a.N >= kManyRows)
-        return launch_top(&tsc::logprob_kernel<DT, kSmall, kEnt, false>, a, a.N, kSmall, false, whole, s);
-    }
-    return launch_top(&tsc::logprob_kernel<DT, tsc::kTopThreads, kEnt, kTop>, a, a.N, tsc::kTopThreads, kTop, whole, s);
+    const bool once = read_once(a, DT == TSC_DTYPE_F32 ? 4 : 2);
+    if (a.N >= kManyRows)
+      return once ? launch_rows<DT, kMany, kEnt, kTop, true>(a, s) : launch_rows<DT, kMany, kEnt, kTop, false>(a, s);
+    return once ? launch_rows<DT, kLarge, kEnt, kTop, true>(a, s) : launch_rows<DT, kLarge, kEnt, kTop, false>(a, s);
   }
+  static std::atomic<uint64_t> slice{0}, join{0};
   const hipError_t err =
-      launch_top(&tsc::logprob_slice_kernel<DT, kEnt, kTop>, a, a.N * a.slices, tsc::kTopThreads, kTop, slice, s);
+      launch_top<kLarge>(&tsc::logprob_slice_kernel<DT, kEnt, kTop>, a, a.N * a.slices, kTop, slice, s);
   if (err != hipSuccess) return err;
-  return launch_top(&tsc::logprob_join_kernel<DT, kEnt, kTop>, a, a.N, kTop ? tsc::kTopThreads : tsc::kWaveSize, kTop,
-                    join, s);
+  return launch_top<kTop ? kLarge : tsc::kWaveSize>(&tsc::logprob_join_kernel<DT, kEnt, kTop>, a, a.N, kTop, join, s);
 }
 
 hipError_t launch_pass(const tsc::LogprobArgs& a, int32_t dtype, bool entropy, hipStream_t s) {
@@ -173,9 +189,6 @@ int32_t tsc_token_logprobs(const void* logits, int32_t dtype, int64_t N, int64_t
   a.logprobs = logprobs, a.entropy = entropy, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
   a.row_status = row_status, a.stats = stats;
   set_parts(a, static_cast<char*>(workspace));
-  // Values alone: logits past the caches' size are read nontemporally (4096 rows of 151936 bfloat16 201
-  // us against 212). Not where the backward pass reads them again (85 us against 110 behind that).
-  a.once = stats == nullptr && N * V * (dtype == TSC_DTYPE_F32 ? 4 : 2) > kCacheBytes;
   (void)hipGetLastError();  // start from a clean error state so a launch error is ours
   return launch_pass(a, dtype, entropy != nullptr, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? TSC_OK
                                                                                                        : TSC_ERR_HIP;

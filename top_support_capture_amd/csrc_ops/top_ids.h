@@ -31,27 +31,28 @@ __device__ inline uint64_t piece_bound(uint64_t k) {
   return k == 0 ? 0 : (k >> 32 << 32) | (uint32_t)~(~(uint32_t)k * kPiece + (kPiece - 1));
 }
 
-constexpr int kTopThreads = 1024;
-constexpr int kTopWaves = kTopThreads / kWaveSize;
-constexpr int kTopMost = 128;          // n
-constexpr int kTopFew = 512;           // candidates that are ranked by counting
-constexpr int kTopCap = kTopFew + kTopThreads * 8;  // those, and a round of pieces of 8
-constexpr int kTopPerWave = kTopMost / kTopWaves + 1;
+constexpr int kTopMost = 128;  // n
+constexpr int kTopFew = 512;   // candidates that are ranked by counting
 
-// A workgroup's LDS for the selection: kTopLds bytes of dynamic LDS, and this.
+// The LDS of a selection by kThr threads: kBytes of dynamic LDS, and TopShared.
+template <int kThr>
+struct TopLists {
+  static constexpr int kWaves = kThr / kWaveSize, kGroups = kThr / 16;
+  static constexpr int kCap = kTopFew + kThr * 8;  // those, and a round of pieces of 8
+  static constexpr size_t kBytes = kCap * 8 + kThr * 2;
+  uint64_t* cand;    // [kCap]
+  uint16_t* thread;  // [kThr]
+  __device__ inline explicit TopLists(void* lds)
+      : cand(reinterpret_cast<uint64_t*>(lds)), thread(reinterpret_cast<uint16_t*>(cand + kCap)) {}
+};
+template <int kThr>
 struct TopShared {
-  uint64_t wave[kTopWaves * kTopPerWave];
+  static constexpr int kPerWave = kTopMost / TopLists<kThr>::kWaves + 1;
+  uint64_t wave[TopLists<kThr>::kWaves * kPerWave];
   uint64_t bound;
   uint32_t hist[256];
   uint32_t count, threads, digit, left;
 };
-struct TopLists {
-  uint64_t* cand;   // [kTopCap]
-  uint16_t* thread; // [kTopThreads]
-  __device__ inline explicit TopLists(void* lds)
-      : cand(reinterpret_cast<uint64_t*>(lds)), thread(reinterpret_cast<uint16_t*>(cand + kTopCap)) {}
-};
-constexpr size_t kTopLds = kTopCap * 8 + kTopThreads * 2;
 
 // How many of list[0, c) are greater than `mine`, which 16 neighbouring lanes ask for together: each
 // takes every 16th. (One thread to a key, reading the list by itself, took the largest part of the
@@ -65,12 +66,11 @@ __device__ inline int count_above(const uint64_t* list, int c, uint64_t mine) {
   above += dpp_mov<dpp::kRowRor4>(above, above);
   return above + dpp_mov<dpp::kRowRor8>(above, above);
 }
-constexpr int kTopGroups = kTopThreads / 16;
-
 // The n-th greatest of list[0, c), 0 if there are fewer (keys other than 0 are distinct). Needs
 // sh.bound == 0 and a barrier before, and a barrier behind it.
-__device__ inline void top_nth(const uint64_t* list, int c, int n, TopShared& sh) {
-  for (int g = 0; g < c; g += kTopGroups) {
+template <int kThr>
+__device__ inline void top_nth(const uint64_t* list, int c, int n, TopShared<kThr>& sh) {
+  for (int g = 0; g < c; g += TopLists<kThr>::kGroups) {
     const int i = g + ((int)threadIdx.x >> 4);
     const uint64_t mine = i < c ? list[i] : 0;
     if (count_above(list, c, mine) == n - 1 && mine != 0) sh.bound = mine;
@@ -88,14 +88,16 @@ __device__ inline uint64_t wave_best(uint64_t key) {
 // A key that at least n of the threads' keys reach, near the n-th best: the n-th best among each
 // wave's best few; 0 if those are fewer than n. Where only the first threads have a key (`some`),
 // they are dealt out to all waves first.
-__device__ inline uint64_t top_bound(uint64_t key, int n, bool some, const TopLists& lists, TopShared& sh) {
+template <int kThr>
+__device__ inline uint64_t top_bound(uint64_t key, int n, bool some, const TopLists<kThr>& lists, TopShared<kThr>& sh) {
+  constexpr int kWaves = TopLists<kThr>::kWaves;
   const uint32_t tid = threadIdx.x, w = tid / kWaveSize;
-  const int per = (n + kTopWaves - 1) / kTopWaves + (n > 1 ? 1 : 0);  // at most kTopPerWave
+  const int per = (n + kWaves - 1) / kWaves + (n > 1 ? 1 : 0);  // at most kPerWave
   lds_barrier();  // sh may still be read by an earlier call
   if (some) {
     lists.cand[tid] = key;
     lds_barrier();
-    key = lists.cand[(tid & 15) * kWaveSize + (tid >> 4)];
+    key = lists.cand[(tid % kWaves) * kWaveSize + tid / kWaves];
   }
   for (int i = 0; i < per; ++i) {
     const uint64_t best = wave_best(key);
@@ -104,21 +106,23 @@ __device__ inline uint64_t top_bound(uint64_t key, int n, bool some, const TopLi
   }
   if (tid == 0) sh.bound = 0;
   lds_barrier();
-  top_nth(sh.wave, kTopWaves * per, n, sh);
+  top_nth(sh.wave, kWaves * per, n, sh);
   lds_barrier();
   return sh.bound;
 }
 
-// Leaves the n greatest of cand[0, c) there, in any order, and sh.count = n (n < c <= kTopCap,
+// Leaves the n greatest of cand[0, c) there, in any order, and sh.count = n (n < c <= kCap,
 // all distinct). Digit by digit from the top: a histogram of the keys that share the n-th one's
 // upper digits gives its next digit. Returns the n-th greatest.
-__device__ inline uint64_t top_narrow(uint64_t* cand, int c, int n, TopShared& sh) {
-  constexpr int kE = (kTopCap + kTopThreads - 1) / kTopThreads;
+template <int kThr>
+__device__ inline uint64_t top_narrow(uint64_t* cand, int c, int n, TopShared<kThr>& sh) {
+  constexpr int kE = (TopLists<kThr>::kCap + kThr - 1) / kThr;
+  static_assert(kThr >= 256, "a thread for each digit");
   const int tid = (int)threadIdx.x;
   uint64_t k[kE], prefix = 0;
   lds_barrier();
 #pragma unroll
-  for (int i = 0; i < kE; ++i) k[i] = tid + i * kTopThreads < c ? cand[tid + i * kTopThreads] : 0;
+  for (int i = 0; i < kE; ++i) k[i] = tid + i * kThr < c ? cand[tid + i * kThr] : 0;
   uint32_t left = (uint32_t)n;
   for (int shift = 56; shift >= 0; shift -= 8) {
     if (tid < 256) sh.hist[tid] = 0;
@@ -154,12 +158,13 @@ __device__ inline uint64_t top_narrow(uint64_t* cand, int c, int n, TopShared& s
 
 // The n first of the sh.count candidates in order, and 0 behind them if they are fewer: sh.wave[0, n),
 // once all threads are through.
-__device__ inline const uint64_t* top_sort(uint64_t* cand, int n, TopShared& sh) {
-  static_assert(kTopWaves * kTopPerWave >= kTopMost, "room for the result");
+template <int kThr>
+__device__ inline const uint64_t* top_sort(uint64_t* cand, int n, TopShared<kThr>& sh) {
+  static_assert(sizeof(sh.wave) >= kTopMost * 8 && kThr >= kTopMost, "room for the result");
   lds_barrier();
   if ((int)sh.count > kTopFew) top_narrow(cand, (int)sh.count, n, sh);
   const int c = (int)sh.count, tid = (int)threadIdx.x;
-  for (int g = 0; g < c; g += kTopGroups) {
+  for (int g = 0; g < c; g += TopLists<kThr>::kGroups) {
     const int i = g + (tid >> 4);
     const uint64_t mine = i < c ? cand[i] : 0;
     const int above = count_above(cand, c, mine);
@@ -172,11 +177,11 @@ __device__ inline const uint64_t* top_sort(uint64_t* cand, int n, TopShared& sh)
 
 // The candidates among row[lo, hi), lo a multiple of 8, from the threads' keys (0 of a thread that
 // has read nothing), into lists.cand and sh.count: all of the n first (as many as there are) and
-// few others. Thread t has read the pieces from lo + t pieces on in steps of kTopThreads.
-template <int DT>
+// few others. Thread t has read the pieces from lo + t pieces on in steps of kThr.
+template <int DT, int kThr>
 __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi, uint64_t key, int n,
-                                   const TopLists& lists, TopShared& sh) {
-  constexpr int kSize = Piece<DT>::kSize, kStep = kTopThreads * kSize;
+                                   const TopLists<kThr>& lists, TopShared<kThr>& sh) {
+  constexpr int kSize = Piece<DT>::kSize, kStep = kThr * kSize, kCap = TopLists<kThr>::kCap;
   const uint32_t tid = threadIdx.x;
   const uint64_t threads_bound = top_bound(key, n, hi - lo < kStep, lists, sh);
   uint64_t bound = piece_bound<kSize>(threads_bound);
@@ -187,7 +192,7 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
   const uint32_t steps = (uint32_t)((hi - lo + kStep - 1) / kStep);
   const uint32_t items = sh.threads * steps;  // pieces to read: at most 2^10 * 2^19
   // Item j is piece j % steps of the thread j / steps of the list; from round to round by addition.
-  const uint32_t di = kTopThreads / steps, dr = kTopThreads - di * steps;
+  const uint32_t di = kThr / steps, dr = kThr - di * steps;
   uint32_t i = tid / steps, r = tid - i * steps;
   // kB rounds of pieces from item j0 on, all in flight together; what does not fit is counted.
   auto rounds = [&](uint32_t j0, auto blocks) {
@@ -198,8 +203,8 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
 #pragma unroll
     for (int b = 0; b < kB; ++b) {
       at[b] = hi;
-      if (wave_first + b * kTopThreads < items) {  // the same for the wave
-        if (j0 + b * kTopThreads + tid < items) at[b] = lo + (int64_t)r * kStep + (int64_t)lists.thread[i] * kSize;
+      if (wave_first + b * kThr < items) {  // the same for the wave
+        if (j0 + b * kThr + tid < items) at[b] = lo + (int64_t)r * kStep + (int64_t)lists.thread[i] * kSize;
         Piece<DT> v = Piece<DT>::lowest();
         if (at[b] + kSize <= hi) v = Piece<DT>::load(row + at[b]);
         v.unpack(x[b]);
@@ -210,7 +215,7 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
     const float least = bound == 0 ? -__builtin_inff() : key_value(bound);
 #pragma unroll
     for (int b = 0; b < kB; ++b) {
-      if (wave_first + b * kTopThreads >= items) continue;
+      if (wave_first + b * kThr >= items) continue;
       if (at[b] < hi && at[b] + kSize > hi) load_part<DT>(row, at[b], hi, x[b]);
       uint32_t reach = 0;  // elements that reach the bound's value: few
 #pragma unroll
@@ -223,7 +228,7 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
         const uint64_t k = top_key(v, (uint32_t)(at[b] + e));
         if (k >= bound) {
           const uint32_t to = atomicAdd(&sh.count, 1u);
-          if (to < (uint32_t)kTopCap) lists.cand[to] = k;
+          if (to < (uint32_t)kCap) lists.cand[to] = k;
         }
       }
     }
@@ -234,10 +239,10 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
   };
   constexpr uint32_t kBatch = 2;
   bool fits = true;
-  for (uint32_t j0 = 0; j0 < items && fits; j0 += kBatch * kTopThreads) {
+  for (uint32_t j0 = 0; j0 < items && fits; j0 += kBatch * kThr) {
     const uint32_t have = rounds(j0, std::integral_constant<int, kBatch>());
-    fits = have <= (uint32_t)kTopCap;
-    if (fits && j0 + kBatch * kTopThreads < items && have > (uint32_t)kTopFew)
+    fits = have <= (uint32_t)kCap;
+    if (fits && j0 + kBatch * kThr < items && have > (uint32_t)kTopFew)
       bound = top_narrow(lists.cand, (int)have, n, sh);
   }
   if (fits) return;
@@ -246,24 +251,26 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
   if (tid == 0) sh.count = 0;
   lds_barrier();
   i = tid / steps, r = tid - i * steps;
-  for (uint32_t j0 = 0; j0 < items; j0 += kTopThreads) {
+  for (uint32_t j0 = 0; j0 < items; j0 += kThr) {
     const uint32_t have = rounds(j0, std::integral_constant<int, 1>());
-    if (j0 + kTopThreads < items && have > (uint32_t)kTopFew) bound = top_narrow(lists.cand, (int)have, n, sh);
+    if (j0 + kThr < items && have > (uint32_t)kTopFew) bound = top_narrow(lists.cand, (int)have, n, sh);
   }
 }
 
 // The candidates among the keys of `slices` (at most kMaxSlices) slices in memory, n of each, in
 // order: as above. The n-th best among each slice's first few bounds them.
-__device__ inline void top_collect_keys(const uint64_t* keys, int slices, int n, const TopLists& lists, TopShared& sh) {
+template <int kThr>
+__device__ inline void top_collect_keys(const uint64_t* keys, int slices, int n, const TopLists<kThr>& lists, TopShared<kThr>& sh) {
+  static_assert(TopLists<kThr>::kCap >= kMaxSlices * kTopMost, "every key may be a candidate");
   const int tid = (int)threadIdx.x, count = slices * n;
   const int some = (n + slices - 1) / slices + 2, per = some < n ? some : n;  // slices * per < n + 3 slices
-  for (int i = tid; i < slices * per; i += kTopThreads) lists.cand[i] = keys[i / per * n + i % per];
+  for (int i = tid; i < slices * per; i += kThr) lists.cand[i] = keys[i / per * n + i % per];
   if (tid == 0) sh.bound = 0, sh.count = 0;
   lds_barrier();
   top_nth(lists.cand, slices * per, n, sh);
   lds_barrier();
   const uint64_t bound = sh.bound;
-  for (int i = tid; i < count; i += kTopThreads)  // at most kTopCap
+  for (int i = tid; i < count; i += kThr)  
     if (keys[i] != 0 && keys[i] >= bound) lists.cand[atomicAdd(&sh.count, 1u)] = keys[i];
   lds_barrier();
 }
