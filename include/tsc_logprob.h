@@ -28,7 +28,7 @@ extern "C" {
  * N, V         0 <= N <= 2^21, 1 <= V < 2^31 - 16, and N ceil(V / 2^19) <= 2^21.
  * temperature  [N] float32, normal positive finite, or NULL (1).
  * tokens       [N] int32 in [0, V), or -1 for a row that is padding (what tsc_verify_drafts writes
- *              for a step that emits nothing): its logits are not read, logprob and entropy are 0.
+ *              for a step that emits nothing): nothing in it plays a part, logprob and entropy are 0.
  * top          0..min(V, TSC_MAX_TOP).
  * logprobs     [N] float32 out; -inf for a token whose logit is -inf.
  * entropy      [N] float32 out, in nats, or NULL.

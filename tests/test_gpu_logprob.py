@@ -391,6 +391,33 @@ def test_in_a_graph():
         assert all(torch.equal(p, q) for p, q in zip(got + again, want + want))
 
 
+def test_the_longest_row():
+    # One row of the most elements there are, cut into slices and segments. All but four logits are -12:
+    # s = 1 + e^-1 + 2 e^-2 + (V - 4) e^-52 relative to the maximum.
+    V = 2**31 - 17
+    log(f"case logprobs of one row of {V}")
+    x = torch.full((1, V), -12.0, dtype=torch.bfloat16, device=DEV)
+    at = [V - 1, 2**30 + 3, 5, V - 9]
+    for i, v in zip(at, (40.0, 39.0, 38.0, 38.0)):
+        x[0, i] = v
+    tk, w = torch.tensor([V - 1], dtype=torch.int32, device=DEV), torch.ones(1, device=DEV)
+    s = 1 + math.exp(-1) + 2 * math.exp(-2) + (V - 4) * math.exp(-52)
+    lp = -math.log(s)
+    out = tsc.token_logprobs(x, tk, top=6, return_entropy=True)
+    assert out.top_ids[0].tolist() == [V - 1, 2**30 + 3, 5, V - 9, 0, 1]
+    # Every sum here is within a few roundings of its terms: far inside 2^-18.
+    assert abs(float(out.logprobs[0]) - lp) <= 2.0**-18
+    want = [lp, lp - 1, lp - 2, lp - 2, lp - 52, lp - 52]
+    assert np.allclose(out.top_logprobs[0].tolist(), want, rtol=0, atol=2.0**-18)
+    one = tsc.token_logprobs_grad(x, tk, w)
+    assert float(one.logprobs[0]) == float(out.logprobs[0])
+    g = one.grad_logits[0]
+    p = [math.exp(v) for v in want[:4]]
+    got = g[at].double().cpu().numpy()
+    assert np.allclose(got, [1 - p[0], -p[1], -p[2], -p[3]], rtol=2.0**-8, atol=2.0**-18)
+    assert abs(float(g[2**31 - 100]) + math.exp(want[4])) <= 2.0**-7 * math.exp(want[4])
+
+
 def test_offsets_past_32_bits():
     # Rows whose elements lie more than 2^31 elements into logits and gradient; all but the last two
     # are padding, which is not read and has gradient 0.

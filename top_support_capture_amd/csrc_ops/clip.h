@@ -175,8 +175,9 @@ __device__ inline float clip_factor(const ClipNorm& c, double* sh) {
 }
 
 // In place: nothing to do where the factor is 1. A workgroup takes several units, as many as leave
-// a grid that is soon through when there is nothing to do (each wave of an empty one costs 50 ps:
-// a grid of one unit of 2048 elements each 76 us for 357 million elements).
+// a grid that is soon through when there is nothing to do: each wave of an empty one costs 50 ps, a
+// grid with a unit of 2048 elements each 76 us for 357 million elements, this one 4. (374 million
+// float32 elements scaled take 540 us, 5.5 TB/s; with a unit for each workgroup 515.)
 template <int DT>
 __device__ inline void scale_unit(const NormTable::Part& p, float by) {
   using P = Piece<DT>;

@@ -194,7 +194,7 @@ int32_t tsc_clip_grad_norm(const void* const* tensors, const int64_t* numels, co
   }
   return launched();
 } catch (const std::bad_alloc&) {
-  return TSC_ERR_INVALID_ARGUMENT;
+  return TSC_ERR_UNSUPPORTED;  // no host memory for a list of that length
 }
 
 int32_t tsc_clip_grads(const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int64_t count,
@@ -204,11 +204,12 @@ int32_t tsc_clip_grads(const void* const* tensors, const int64_t* numels, const 
   if (!(max_norm >= 0.0f) || !norm) return TSC_ERR_INVALID_ARGUMENT;
   const Lists l{tensors, numels, dtypes, count, out, out_dtypes};
   if (const int32_t e = check_out(l)) return e;
+  if (count == 0) return TSC_OK;
   (void)hipGetLastError();
   launch_scale(l, {nullptr, 0, max_norm, nullptr, norm}, reinterpret_cast<hipStream_t>(stream));
   return launched();
 } catch (const std::bad_alloc&) {
-  return TSC_ERR_INVALID_ARGUMENT;
+  return TSC_ERR_UNSUPPORTED;  // no host memory for a list of that length
 }
 
 }  // extern "C"

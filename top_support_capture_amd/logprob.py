@@ -139,7 +139,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Opti
 
     ``logits`` [N, V] float32 or bfloat16, ``tokens`` int32 [N], ``temperature`` float32 [N] (None:
     1), ``top`` at most ``MAX_TOP`` and V. A token of -1 marks a row as padding: logprob and entropy
-    0, no gradient, its logits are not read. A row of status other than ROW_OK has top ids -1.
+    0, no gradient, whatever it holds. A row of status other than ROW_OK has top ids -1.
     ``replay_logprob`` is the same over a captured support.
 
     ``logprobs``, ``entropy`` and ``top_logprobs`` are differentiable with respect to ``logits``, in
