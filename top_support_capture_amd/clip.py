@@ -33,19 +33,22 @@ def _dense(t: torch.Tensor) -> bool:
 def _listed(tensors: Tensors, name: str):
     """(tensors, dtype codes) of a checked list."""
     tensors = (tensors,) if isinstance(tensors, torch.Tensor) else tuple(tensors)
-    try:
-        dtypes = array("i", [_DTYPES[t.dtype] for t in tensors])
-    except (KeyError, AttributeError):
-        raise ValueError(f"{name} must be float32 or bfloat16 tensors") from None
+    if not all(isinstance(t, torch.Tensor) for t in tensors):
+        raise ValueError(f"{name} must be tensors")
+    codes, grad, strided = [], torch.is_grad_enabled(), torch.strided
     dev = tensors[0].device if tensors else None
-    if any(t.device != dev for t in tensors) or (tensors and dev.type != "cuda"):
-        raise ValueError(f"{name} must be on one GPU")
-    if (any(t.layout is not torch.strided for t in tensors)
-            or not (all(map(torch.Tensor.is_contiguous, tensors)) or all(map(_dense, tensors)))):
-        raise ValueError(f"{name} must be dense: without gaps or elements that share their place")
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise ValueError(f"{name} must not ask for gradients (detach them): the norm and the clipping have none")
-    return tensors, dtypes
+    for t in tensors:
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{name} must be float32 or bfloat16")
+        codes.append(code)
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"{name} must be on one GPU")
+        if t.layout is not strided or not (t.is_contiguous() or _dense(t)):
+            raise ValueError(f"{name} must be dense: without gaps or elements that share their place")
+        if grad and t.requires_grad:
+            raise ValueError(f"{name} must not ask for gradients (detach them): the norm and the clipping have none")
+    return tensors, array("i", codes)
 
 
 def _bound(max_norm) -> float:
