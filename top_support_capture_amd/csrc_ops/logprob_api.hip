@@ -13,9 +13,13 @@ static_assert(TSC_MAX_TOP == tsc::kTopMost, "the selection's lists hold that man
 
 // Whole rows for a workgroup each when there are rows enough, or short ones; slices otherwise, as
 // many as the chip holds at once (two workgroups on each CU), of 8192 elements at least, and whole
-// steps of a workgroup for either type.
-Cut pass_cut(int64_t N, int64_t V) {
-  if (N >= 128 || V <= 65536) return {1, V};
+// steps of a workgroup for either type. Slices cost a second launch, and with alternatives a second
+// selection. Sliced against whole, us, without / with 5 alternatives and the entropy: bf16 of 151936, 1
+// row 7.1 / 13.6 against 11.5 / 18.4, 64 rows 11.4 / 20.3 against 13.1 / 20.2, 128 rows 15.8 / 24.8
+// against 13.6 / 20.9; float32 of 129280, 100 rows 15.1 / 23.2 against 13.6 / 19.9, of 262144, 64 rows
+// 16.1 / 23.4 against 20.8 / 30.1; bf16 of 65536, 16 rows 7.5 / 13.7 against 6.7 / 11.7.
+Cut pass_cut(int64_t N, int64_t V, int32_t top) {
+  if (N >= 128 || V <= 65536 || (top > 0 && N >= 64 && V <= 160000)) return {1, V};
   const int64_t most = ceil_div(V, 8192) < tsc::kMaxSlices ? ceil_div(V, 8192) : tsc::kMaxSlices;
   const int64_t n = 512 / (N > 0 ? N : 1) < most ? 512 / (N > 0 ? N : 1) : most;
   const int64_t len = ceil_div(ceil_div(V, n), 4096) * 4096;
@@ -50,13 +54,13 @@ int64_t parts_bytes(int64_t N, const Cut& cut) {
 }
 
 int64_t pass_bytes(int64_t N, int64_t V, int32_t top) {
-  const Cut cut = pass_cut(N, V);
+  const Cut cut = pass_cut(N, V, top);
   return cut.n > 1 ? parts_bytes(N, cut) + round16(N * cut.n * top * 8) : 0;
 }
 
 // Slices' states and keys from `ws` on.
 void set_parts(tsc::LogprobArgs& a, char* ws) {
-  const Cut cut = pass_cut(a.N, a.V);
+  const Cut cut = pass_cut(a.N, a.V, a.top);
   a.slices = cut.n, a.slice_len = cut.len;
   a.parts = reinterpret_cast<tsc::LogprobPart*>(ws);
   a.keys = reinterpret_cast<uint64_t*>(ws + parts_bytes(a.N, cut));
