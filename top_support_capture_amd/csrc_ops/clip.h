@@ -73,7 +73,9 @@ struct ClipTable {
 };
 
 using NormTable = ClipTable<304, 8192, false>;
-using ScaleTable = ClipTable<184, 2048, true>;
+// Two loads a thread of kE elements each.
+template <int kE>
+using ScaleTable = ClipTable<184, 2 * kClipThreads * kE, true>;
 
 // Pieces of a thread in a unit of the norm's table.
 template <int DT>
@@ -219,10 +221,10 @@ __global__ void __launch_bounds__(kClipThreads, 8) clip_in_place_kernel(NormTabl
   }
 }
 
-// Into other tensors: a unit per workgroup, 8 elements a thread, which is near what the memory does
-// fastest. 1.12 billion elements from bfloat16 to float32 (6.7 GB) take 1060 us, 6.3 TB/s; 4 elements
-// a thread 1440 (its load waits for the table's), 16 1075 to 1140, 32 1200; a contiguous span for
-// each of 1024 workgroups and 16-byte stores 32 bytes apart 1850.
+// Into other tensors: a unit per workgroup and two loads a thread, near what the memory does fastest.
+// 1.12 billion elements from bfloat16 to float32 (6.7 GB) take 1060 us, 6.3 TB/s; one load a thread 1440
+// (it waits for the table's), four 1140; a contiguous span for each of 1024 workgroups and 16-byte
+// stores 32 bytes apart 1850. 128 million from bfloat16 to bfloat16 84 us, 6.4 TB/s, with one load 89.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_by2 __attribute__((aligned(2)));
 
@@ -254,12 +256,12 @@ __device__ inline void store_few(typename Row<OT>::Bits* p, const float (&v)[kE]
 
 // The values are asked for before the factor is, which comes from memory too.
 template <int DT, int OT, int kE, class Factor>
-__device__ inline void copy_unit(const ScaleTable::Part& p, Factor factor) {
-  constexpr int kU = ScaleTable::kUnitSize / (kClipThreads * kE), kStep = kClipThreads * kE;
+__device__ inline void copy_unit(const typename ScaleTable<kE>::Part& p, Factor factor) {
+  constexpr int kStep = kClipThreads * kE, kU = 2;
   const auto* x = (const typename Row<DT>::Bits*)p.src;
   auto* y = (typename Row<OT>::Bits*)p.dst;
   const int64_t at = p.lo + (int64_t)threadIdx.x * kE;
-  if (p.hi - p.lo == ScaleTable::kUnitSize) {
+  if (p.hi - p.lo == ScaleTable<kE>::kUnitSize) {
     float v[kU][kE];
 #pragma unroll
     for (int u = 0; u < kU; ++u) load_few<DT, kE>(x + at + u * kStep, v[u]);
@@ -279,9 +281,9 @@ __device__ inline void copy_unit(const ScaleTable::Part& p, Factor factor) {
   }
 }
 
-// kE 8: a table of bfloat16 tensors with bfloat16 results; 4: any.
+// kE 8: bfloat16 tensors with bfloat16 results; 4: any.
 template <int kE>
-__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(ScaleTable a, ClipNorm c) {
+__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(ScaleTable<kE> a, ClipNorm c) {
   constexpr int F = TSC_DTYPE_F32, B = TSC_DTYPE_BF16;
   __shared__ double sh[kClipWaves];
   float by = 0.0f;

@@ -109,34 +109,36 @@ void launch_join(const double* partials, int64_t n, float* norm, hipStream_t s) 
   hipLaunchKernelGGL(tsc::clip_join_kernel, dim3(1), dim3(tsc::kClipThreads), 0, s, partials, (int32_t)n, norm);
 }
 
-bool in_place(const Lists& l) {
-  for (int64_t i = 0; i < l.count; ++i)
-    if (l.numels[i] > 0 && !l.own(i)) return false;
-  return true;
+template <int kE>
+int64_t launch_copy(const Lists& l, int64_t from, const tsc::ClipNorm& c, hipStream_t s) {
+  tsc::ScaleTable<kE> t;
+  const int64_t to = fill(t, l, from);
+  if (t.n > 0)
+    hipLaunchKernelGGL(tsc::clip_scale_kernel<kE>, dim3((unsigned)groups(t, kMaxRows)), dim3(tsc::kClipThreads), 0, s, t, c);
+  return to;
+}
+
+int64_t launch_in_place(const Lists& l, int64_t from, const tsc::ClipNorm& c, hipStream_t s) {
+  tsc::NormTable t;
+  const int64_t to = fill(t, l, from);
+  if (t.n > 0)
+    hipLaunchKernelGGL(tsc::clip_in_place_kernel, dim3((unsigned)groups(t, tsc::kInPlaceGroups)), dim3(tsc::kClipThreads), 0,
+                       s, t, c);
+  return to;
 }
 
 void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
-  const bool own = in_place(l);
+  bool own = true, narrow = true;
+  for (int64_t i = 0; i < l.count; ++i) {
+    if (l.numels[i] == 0) continue;
+    own = own && l.own(i);
+    narrow = narrow && l.dtypes[i] == TSC_DTYPE_BF16 && l.out_dtype(i) == TSC_DTYPE_BF16;
+  }
   for (int64_t i = 0; i < l.count;) {
-    if (own) {
-      tsc::NormTable t;
-      i = fill(t, l, i);
-      if (t.n == 0) break;
-      hipLaunchKernelGGL(tsc::clip_in_place_kernel, dim3((unsigned)groups(t, tsc::kInPlaceGroups)),
-                         dim3(tsc::kClipThreads), 0, s, t, c);
-    } else {
-      tsc::ScaleTable t;
-      const int64_t from = i;
-      i = fill(t, l, i);
-      if (t.n == 0) break;
-      bool narrow = true;
-      for (int64_t k = from; k < i; ++k)
-        narrow = narrow && (l.numels[k] == 0 || (l.dtypes[k] == TSC_DTYPE_BF16 && l.out_dtype(k) == TSC_DTYPE_BF16));
-      const dim3 grid((unsigned)groups(t, kMaxRows));
-      if (narrow) hipLaunchKernelGGL(tsc::clip_scale_kernel<8>, grid, dim3(tsc::kClipThreads), 0, s, t, c);
-      else hipLaunchKernelGGL(tsc::clip_scale_kernel<4>, grid, dim3(tsc::kClipThreads), 0, s, t, c);
-    }
-    c.norm_out = nullptr;  // written once
+    const int64_t from = i;
+    i = own ? launch_in_place(l, from, c, s) : narrow ? launch_copy<8>(l, from, c, s) : launch_copy<4>(l, from, c, s);
+    for (int64_t k = from; k < i; ++k)
+      if (l.numels[k] > 0) c.norm_out = nullptr;  // written by the first launch
   }
 }
 
@@ -144,7 +146,7 @@ void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
 // launch: few of either.
 bool joins_inline(const Lists& l, int64_t partials) {
   int64_t units = 0;
-  for (int64_t i = 0; i < l.count; ++i) units += ceil_div(l.numels[i], tsc::ScaleTable::kUnitSize);
+  for (int64_t i = 0; i < l.count; ++i) units += ceil_div(l.numels[i], 2048);
   return partials > 0 && partials * units <= kJoinInline;
 }
 
