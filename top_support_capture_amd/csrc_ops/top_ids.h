@@ -6,6 +6,10 @@
 // among the n best keys: each better key stands for an element that precedes every element of the
 // thread. So a bound below the n-th best key leaves few threads, whose pieces are read once more and
 // compared with the bound; what reaches it is ranked.
+//
+// All of it is a chain of short steps between barriers. For 256 rows of 151936 bfloat16 logits it adds
+// 3.6 us to a pass of 16.4 for one alternative, 4 for 20, 8 for 64 and 14 for 128 (waves' best, ranks
+// and pieces all grow with n); with rows enough other workgroups' loads cover most of it.
 #pragma once
 
 #include "piece.h"
@@ -66,6 +70,7 @@ __device__ inline int count_above(const uint64_t* list, int c, uint64_t mine) {
   above += dpp_mov<dpp::kRowRor4>(above, above);
   return above + dpp_mov<dpp::kRowRor8>(above, above);
 }
+
 // The n-th greatest of list[0, c), 0 if there are fewer (keys other than 0 are distinct). Needs
 // sh.bound == 0 and a barrier before, and a barrier behind it.
 template <int kThr>
@@ -89,7 +94,8 @@ __device__ inline uint64_t wave_best(uint64_t key) {
 // wave's best few; 0 if those are fewer than n. Where only the first threads have a key (`some`),
 // they are dealt out to all waves first.
 template <int kThr>
-__device__ inline uint64_t top_bound(uint64_t key, int n, bool some, const TopLists<kThr>& lists, TopShared<kThr>& sh) {
+__device__ inline uint64_t top_bound(uint64_t key, int n, bool some, const TopLists<kThr>& lists,
+                                     TopShared<kThr>& sh) {
   constexpr int kWaves = TopLists<kThr>::kWaves;
   const uint32_t tid = threadIdx.x, w = tid / kWaveSize;
   const int per = (n + kWaves - 1) / kWaves + (n > 1 ? 1 : 0);  // at most kPerWave
@@ -260,7 +266,8 @@ __device__ inline void top_collect(const typename Row<DT>::Bits* row, int64_t lo
 // The candidates among the keys of `slices` (at most kMaxSlices) slices in memory, n of each, in
 // order: as above. The n-th best among each slice's first few bounds them.
 template <int kThr>
-__device__ inline void top_collect_keys(const uint64_t* keys, int slices, int n, const TopLists<kThr>& lists, TopShared<kThr>& sh) {
+__device__ inline void top_collect_keys(const uint64_t* keys, int slices, int n, const TopLists<kThr>& lists,
+                                        TopShared<kThr>& sh) {
   static_assert(TopLists<kThr>::kCap >= kMaxSlices * kTopMost, "every key may be a candidate");
   const int tid = (int)threadIdx.x, count = slices * n;
   const int some = (n + slices - 1) / slices + 2, per = some < n ? some : n;  // slices * per < n + 3 slices
@@ -270,7 +277,7 @@ __device__ inline void top_collect_keys(const uint64_t* keys, int slices, int n,
   top_nth(lists.cand, slices * per, n, sh);
   lds_barrier();
   const uint64_t bound = sh.bound;
-  for (int i = tid; i < count; i += kThr)  
+  for (int i = tid; i < count; i += kThr)
     if (keys[i] != 0 && keys[i] >= bound) lists.cand[atomicAdd(&sh.count, 1u)] = keys[i];
   lds_barrier();
 }
