@@ -111,6 +111,32 @@ def test_prepared_and_partly_in_place():
     assert all(torch.all(o == 0.125) for o in out)
 
 
+@pytest.mark.parametrize("dtype,to", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("order", ["as they lie", "shuffled"])
+def test_flat_buffers(dtype, to, order):
+    # Tensors and results lie alike in two buffers, more of them than a launch takes; and not quite alike.
+    log(f"case clip of flat buffers {dtype} to {to}, {order}")
+    rng = np.random.default_rng(12)
+    sizes = rng.integers(1, 5000, 700)
+    n = int(sizes.sum())
+    flat = torch.from_numpy(rng.standard_normal(n + 1).astype(np.float32)).to(DT[dtype]).to(DEV)[1:]
+    out = torch.full((n + 3,), float("nan"), dtype=DT[to], device=DEV)
+    grads, outs = list(flat.split(sizes.tolist())), list(out[2 : n + 2].split(sizes.tolist()))
+    perm = rng.permutation(700) if order == "shuffled" else np.arange(700)
+    grads, outs = [grads[k] for k in perm], [outs[k] for k in perm]
+    exact = flat.double().cpu().numpy()
+    norm, (want,) = oracle.clip_grads([exact], 3.0)
+    check_norm(tsc.clip_grad_norm(grads, 3.0, out=outs), norm)
+    check_clipped([out[2 : n + 2]], [exact], norm, [want])
+    assert torch.isnan(out[[0, 1, n + 2]]).all()
+    apart = torch.full((int(sizes[perm[350]]),), float("nan"), dtype=DT[to], device=DEV)
+    out.fill_(float("nan"))
+    outs[350] = apart
+    check_norm(tsc.clip_grad_norm(grads, 3.0, out=outs), norm)
+    one = [g.double().cpu().numpy() for g in grads]
+    check_clipped(outs, one, norm, [g * 3.0 / norm for g in one])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_norms_that_are_no_numbers(bad):
     log(f"case clip with {bad}")

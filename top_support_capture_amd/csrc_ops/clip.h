@@ -16,16 +16,22 @@ constexpr int kClipGroups = 2048;  // of a norm's launch, at most: 8 workgroups 
 
 // Up to kN tensors in units of kUnit elements. kN is bounded by the 4 KB that a kernel's arguments
 // may take: a tensor's address, type and the size of its last unit share a word.
-template <int kN, int kUnit, bool kOut>
+enum class ClipOut {
+  kSelf,  // results in place
+  kEach,  // an address each
+  kFlat,  // one type each for tensors and results, and all results as far from each other as the tensors
+};
+
+template <int kN, int kUnit, ClipOut kOut>
 struct ClipTable {
   static constexpr int kSize = kN;
   static constexpr int64_t kUnitSize = kUnit;
   static constexpr int kHints = 32;
   static_assert(kUnit <= 8192, "13 bits of the word");
   uint64_t src[kN];
-  uint64_t dst[kOut ? kN : 1];  // the address and the type
-  uint32_t first[kN + 1];       // units before each tensor; the last: all
-  uint32_t hint[kHints];        // the tensor of unit i << hint_shift (whole words: scalar loads)
+  uint64_t dst[kOut == ClipOut::kEach ? kN : 1];  // the address and the type; kFlat: their distance
+  uint32_t first[kN + 1];                         // units before each tensor; the last: all
+  uint32_t hint[kHints];  // the tensor of unit i << hint_shift (whole words: scalar loads)
   uint32_t units, hint_shift;
   int32_t n;
 
@@ -43,10 +49,22 @@ struct ClipTable {
   __device__ inline Part part(uint32_t unit) const {
     uint32_t t = hint[unit >> hint_shift];
     while (first[t + 1] <= unit) ++t;
-    const uint64_t s = src[t], d = kOut ? dst[t] : s;
+    const uint64_t s = src[t];
+    uint64_t d = s;
+    if constexpr (kOut == ClipOut::kEach) d = dst[t];
+    if constexpr (kOut == ClipOut::kFlat) {
+      const uint64_t at = s & kAddress, to = dst[0] & kF32;
+      d = (((s & kF32) ? at >> 2 : at >> 1) << (to ? 2 : 1)) + (dst[0] & kAddress);
+      d = (d & kAddress) | to;
+    }
     const int64_t lo = (int64_t)(unit - first[t]) * kUnit;
     const int64_t size = unit + 1 == first[t + 1] ? (int64_t)(s >> 48 & 0x1FFF) + 1 : kUnit;
     return {address(s), address(d), lo, lo + size, (s & kF32) != 0, (d & kF32) != 0};
+  }
+
+  // What a result's address has over its tensor's, counted in elements from 0 and in the result's size.
+  static uint64_t distance(const void* tensor, bool f32, const void* out, bool to_f32) {
+    return reinterpret_cast<uint64_t>(out) - (reinterpret_cast<uint64_t>(tensor) >> (f32 ? 2 : 1) << (to_f32 ? 2 : 1));
   }
 
   // The host's side: an empty table, a tensor of `numel` > 0 more (false: it is full), the end.
@@ -55,7 +73,8 @@ struct ClipTable {
     if (n == kN) return false;
     const uint64_t last = (uint64_t)((numel - 1) % kUnit);
     src[n] = reinterpret_cast<uint64_t>(tensor) | last << 48 | (f32 ? kF32 : 0);
-    if (kOut) dst[n] = reinterpret_cast<uint64_t>(out) | (to_f32 ? kF32 : 0);
+    if constexpr (kOut == ClipOut::kEach) dst[n] = reinterpret_cast<uint64_t>(out) | (to_f32 ? kF32 : 0);
+    if constexpr (kOut == ClipOut::kFlat) dst[0] = (distance(tensor, f32, out, to_f32) & kAddress) | (to_f32 ? kF32 : 0);
     first[n + 1] = first[n] + (uint32_t)((numel + kUnit - 1) / kUnit);
     ++n;
     return true;
@@ -72,10 +91,10 @@ struct ClipTable {
   }
 };
 
-using NormTable = ClipTable<304, 8192, false>;
+using NormTable = ClipTable<304, 8192, ClipOut::kSelf>;
 // Two loads a thread of kE elements each.
-template <int kE>
-using ScaleTable = ClipTable<184, 2 * kClipThreads * kE, true>;
+template <int kE, ClipOut kOut>
+using ScaleTable = ClipTable<kOut == ClipOut::kFlat ? 300 : 184, 2 * kClipThreads * kE, kOut>;
 
 // Pieces of a thread in a unit of the norm's table.
 template <int DT>
@@ -255,14 +274,14 @@ __device__ inline void store_few(typename Row<OT>::Bits* p, const float (&v)[kE]
 }
 
 // The values are asked for before the factor is, which comes from memory too.
-template <int DT, int OT, int kE, class Factor>
-__device__ inline void copy_unit(const typename ScaleTable<kE>::Part& p, Factor factor) {
+template <int DT, int OT, int kE, class Part, class Factor>
+__device__ inline void copy_unit(const Part& p, Factor factor) {
   constexpr int kStep = kClipThreads * kE, kU = 2;
   const auto* x = (const typename Row<DT>::Bits*)p.src;
   auto* y = (typename Row<OT>::Bits*)p.dst;
   const int64_t at = p.lo + (int64_t)threadIdx.x * kE;
-  if (p.hi - p.lo == ScaleTable<kE>::kUnitSize) {
-    float v[kU][kE];
+  float v[kU][kE];
+  if (p.hi - p.lo == kU * kStep) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) load_few<DT, kE>(x + at + u * kStep, v[u]);
     const float by = factor();
@@ -275,15 +294,23 @@ __device__ inline void copy_unit(const typename ScaleTable<kE>::Part& p, Factor 
   } else {
     const float by = factor();
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
-      for (int64_t i = at + u * kStep; i < at + u * kStep + kE && i < p.hi; ++i)
-        Row<OT>::put(y + i, Row<DT>::get(x + i) * by);
+    for (int u = 0; u < kU; ++u) {
+      const int64_t here = at + u * kStep;
+      if (here + kE <= p.hi) {
+        load_few<DT, kE>(x + here, v[u]);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) v[u][e] *= by;
+        store_few<OT, kE>(y + here, v[u]);
+      } else {
+        for (int64_t i = here; i < p.hi; ++i) Row<OT>::put(y + i, Row<DT>::get(x + i) * by);
+      }
+    }
   }
 }
 
 // kE 8: bfloat16 tensors with bfloat16 results; 4: any.
-template <int kE>
-__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(ScaleTable<kE> a, ClipNorm c) {
+template <int kE, ClipOut kOut>
+__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(ScaleTable<kE, kOut> a, ClipNorm c) {
   constexpr int F = TSC_DTYPE_F32, B = TSC_DTYPE_BF16;
   __shared__ double sh[kClipWaves];
   float by = 0.0f;

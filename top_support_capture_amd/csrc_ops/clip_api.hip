@@ -109,12 +109,13 @@ void launch_join(const double* partials, int64_t n, float* norm, hipStream_t s) 
   hipLaunchKernelGGL(tsc::clip_join_kernel, dim3(1), dim3(tsc::kClipThreads), 0, s, partials, (int32_t)n, norm);
 }
 
-template <int kE>
+template <int kE, tsc::ClipOut kOut>
 int64_t launch_copy(const Lists& l, int64_t from, const tsc::ClipNorm& c, hipStream_t s) {
-  tsc::ScaleTable<kE> t;
+  tsc::ScaleTable<kE, kOut> t;
   const int64_t to = fill(t, l, from);
   if (t.n > 0)
-    hipLaunchKernelGGL(tsc::clip_scale_kernel<kE>, dim3((unsigned)groups(t, kMaxRows)), dim3(tsc::kClipThreads), 0, s, t, c);
+    hipLaunchKernelGGL((tsc::clip_scale_kernel<kE, kOut>), dim3((unsigned)groups(t, kMaxRows)), dim3(tsc::kClipThreads), 0,
+                       s, t, c);
   return to;
 }
 
@@ -128,15 +129,27 @@ int64_t launch_in_place(const Lists& l, int64_t from, const tsc::ClipNorm& c, hi
 }
 
 void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
-  bool own = true, narrow = true;
+  // Tensors of one type whose results lie as they do themselves, as in two flat buffers, need no
+  // addresses for the results: more tensors to a launch (224 of 24 MB in all take one, 11 us, instead of
+  // two, 10 and 5).
+  bool own = true, narrow = true, flat = true;
+  uint64_t distance = 0;
+  int64_t first = -1;
   for (int64_t i = 0; i < l.count; ++i) {
     if (l.numels[i] == 0) continue;
+    const bool f32 = l.dtypes[i] == TSC_DTYPE_F32, to_f32 = l.out_dtype(i) == TSC_DTYPE_F32;
+    const uint64_t d = tsc::NormTable::distance(l.src[i], f32, reinterpret_cast<void*>(l.out_begin(i)), to_f32);
+    if (first < 0) first = i, distance = d;
     own = own && l.own(i);
-    narrow = narrow && l.dtypes[i] == TSC_DTYPE_BF16 && l.out_dtype(i) == TSC_DTYPE_BF16;
+    narrow = narrow && !f32 && !to_f32;
+    flat = flat && d == distance && l.dtypes[i] == l.dtypes[first] && l.out_dtype(i) == l.out_dtype(first);
   }
+  constexpr auto kEach = tsc::ClipOut::kEach, kFlat = tsc::ClipOut::kFlat;
   for (int64_t i = 0; i < l.count;) {
     const int64_t from = i;
-    i = own ? launch_in_place(l, from, c, s) : narrow ? launch_copy<8>(l, from, c, s) : launch_copy<4>(l, from, c, s);
+    if (own) i = launch_in_place(l, from, c, s);
+    else if (narrow) i = flat ? launch_copy<8, kFlat>(l, from, c, s) : launch_copy<8, kEach>(l, from, c, s);
+    else i = flat ? launch_copy<4, kFlat>(l, from, c, s) : launch_copy<4, kEach>(l, from, c, s);
     for (int64_t k = from; k < i; ++k)
       if (l.numels[k] > 0) c.norm_out = nullptr;  // written by the first launch
   }
