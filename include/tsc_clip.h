@@ -22,7 +22,8 @@ extern "C" {
 #endif
 
 /*
- * tsc_grad_norm -- norm [1] float32 out: 0 without elements; NaN or +inf where the elements are.
+ * tsc_grad_norm -- norm [1] float32 out: 0 without elements; NaN or +inf where the elements are, and
+ *              +inf past float32's range.
  * workspace    16-byte aligned, at least tsc_grad_norm_workspace(count) bytes; its contents need no
  *              preparation; calls that may run at the same time must not share one.
  */
@@ -33,13 +34,14 @@ int32_t tsc_grad_norm(const void* const* tensors, const int64_t* numels, const i
 size_t tsc_grad_norm_workspace(int64_t count);
 
 /*
- * tsc_clip_grad_norm -- the norm, and every gradient times max_norm / norm where norm > max_norm.
+ * tsc_clip_grad_norm -- the norm, and every gradient times max_norm / norm where norm > max_norm. The
+ * factor is a float32: below 2^-126 it loses digits, and below 2^-149 it is 0.
  * A norm that is NaN or infinite leaves the values as they are (look at `norm` to skip the step).
  * max_norm     >= 0, not NaN.
  * out, out_dtypes  as `tensors` and `dtypes`, of the same sizes: where the results go, rounded
  *              once, to nearest even; NULL, NULL: in place. out[i] may be tensors[i] itself, of the
- *              same dtype. Otherwise no result may overlap another or any gradient
- *              (TSC_ERR_INVALID_ARGUMENT).
+ *              same dtype. Otherwise no result may overlap another or any gradient, and `norm`
+ *              none of either (TSC_ERR_INVALID_ARGUMENT).
  */
 int32_t tsc_clip_grad_norm(const void* const* tensors, const int64_t* numels, const int32_t* dtypes,
                            int64_t count, void* const* out, const int32_t* out_dtypes,

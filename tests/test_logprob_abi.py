@@ -143,6 +143,15 @@ def test_overlaps_are_refused(lib, which, kw):
     assert clip(lib, which=which, **kw) == 1
 
 
+@pytest.mark.parametrize("which", ["clip", "scale"])
+@pytest.mark.parametrize("kw", [
+    dict(norm=0x1000), dict(norm=0x101C), dict(norm=0x2004), dict(norm=0x200E),
+    dict(norm=0x3000, out=(0x3000, 0x4000), out_dtypes=(0, 1)), dict(norm=0x400C, out=(0x3000, 0x4000), out_dtypes=(0, 1)),
+    dict(norm=0x1000, out=(0x3000, 0x4000), out_dtypes=(0, 1))])
+def test_a_norm_in_a_tensor_is_refused(lib, which, kw):
+    assert clip(lib, which=which, **kw) == 1
+
+
 def test_clip_workspaces(lib):
     size = lib.tsc_grad_norm_workspace
     assert size(0) == size(-1) == size(2**20 + 1) == 0

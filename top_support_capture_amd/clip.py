@@ -168,5 +168,5 @@ def clip_grad_norm(tensors: Tensors, max_norm: float, out: Optional[Tensors] = N
 def clip_grads(tensors: Tensors, norm: torch.Tensor, max_norm: float, out: Optional[Tensors] = None,
                stream: Optional[torch.cuda.Stream] = None) -> None:
     """The scaling of ``clip_grad_norm`` by a norm that is known: that of all ranks' gradients, from
-    the root of the sum of the squares of their ``grad_norm``."""
+    the root of the sum of the squares of their ``grad_norm``. ``norm`` lies in none of the tensors."""
     PreparedGrads(tensors, out).scale(norm, max_norm, stream)

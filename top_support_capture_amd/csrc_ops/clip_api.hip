@@ -47,17 +47,20 @@ struct Lists {
   bool own(int64_t i) const { return out_begin(i) == begin(i) && out_dtype(i) == dtypes[i]; }
 };
 
-// Results that no other result and no gradient but their own overlaps.
-int32_t check_out(const Lists& l) {
+// Results that no other result and no gradient but their own overlaps, and a norm that lies in none of
+// either: workgroups read it, or write it, while others write results.
+int32_t check_out(const Lists& l, const float* norm) {
   if ((l.dst == nullptr) != (l.dst_dtypes == nullptr)) return TSC_ERR_INVALID_ARGUMENT;
   if (l.dst) {
     if (const int32_t e = check_list(const_cast<const void* const*>(l.dst), l.numels, l.dst_dtypes, l.count)) return e;
   }
+  const uintptr_t nb = reinterpret_cast<uintptr_t>(norm), ne = nb + sizeof(float);
   std::vector<std::pair<uintptr_t, uintptr_t>> written;
   written.reserve((size_t)l.count);
   bool sorted = true;
   for (int64_t i = 0; i < l.count; ++i) {
     if (l.numels[i] == 0) continue;
+    if ((l.out_begin(i) < ne && nb < l.out_end(i)) || (l.begin(i) < ne && nb < l.end(i))) return TSC_ERR_INVALID_ARGUMENT;
     if (!written.empty() && l.out_begin(i) < written.back().first) sorted = false;
     written.emplace_back(l.out_begin(i), l.out_end(i));
   }
@@ -195,7 +198,7 @@ int32_t tsc_clip_grad_norm(const void* const* tensors, const int64_t* numels, co
   if (const int32_t e = check_list(tensors, numels, dtypes, count)) return e;
   if (!(max_norm >= 0.0f)) return TSC_ERR_INVALID_ARGUMENT;
   const Lists l{tensors, numels, dtypes, count, out, out_dtypes};
-  if (const int32_t e = check_out(l)) return e;
+  if (const int32_t e = check_out(l, norm)) return e;
   if (const int32_t e = check_norm(norm, count, workspace, workspace_bytes)) return e;
   (void)hipGetLastError();
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -218,7 +221,7 @@ int32_t tsc_clip_grads(const void* const* tensors, const int64_t* numels, const 
   if (const int32_t e = check_list(tensors, numels, dtypes, count)) return e;
   if (!(max_norm >= 0.0f) || !norm) return TSC_ERR_INVALID_ARGUMENT;
   const Lists l{tensors, numels, dtypes, count, out, out_dtypes};
-  if (const int32_t e = check_out(l)) return e;
+  if (const int32_t e = check_out(l, norm)) return e;
   if (count == 0) return TSC_OK;
   (void)hipGetLastError();
   launch_scale(l, {nullptr, 0, max_norm, nullptr, norm}, reinterpret_cast<hipStream_t>(stream));
