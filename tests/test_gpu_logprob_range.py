@@ -1,0 +1,63 @@
+"""Token logprobs and their gradient over the whole range of temperatures and logits that the header
+takes (needs an MI355X): from the least normal temperature to the largest finite one, logits up to the
+ends of their type. Bounds as in test_gpu_logprob.py, whose checks are used. Every case prints its name
+before touching the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import top_support_capture_amd as tsc
+from tests.gpu_helpers import log
+from tests.ops_helpers import DEV, DT, tensor
+from tests.test_gpu_logprob import Case, backward, check_grad, check_values
+
+pytestmark = pytest.mark.gpu
+LEAST = float(np.finfo(np.float32).tiny)
+B = 2.0 ** 80
+
+
+def check_all(x, dtype, T, tokens, c, top):
+    xt = torch.from_numpy(x).to(DT[dtype]).to(DEV)
+    exact = xt.double().cpu().numpy()
+    tk, tt = tensor(tokens, torch.int32), tensor(T, torch.float32)
+    leaf = xt.detach().requires_grad_()
+    out = tsc.token_logprobs(leaf, tk, tt, top=top, return_entropy=True)
+    rows = check_values(exact, T, tokens, top, out)
+    assert all(r.status == 0 for r in rows)
+    check_grad(exact, dtype, T, tokens, rows, c, backward(leaf, out, c))
+    c.u = None
+    one = tsc.token_logprobs_grad(xt, tk, tensor(c.a, torch.float32), tt, grad_entropy=tensor(c.b, torch.float32))
+    check_values(exact, T, tokens, 0, one)
+    check_grad(exact, dtype, T, tokens, rows, c, one.grad_logits)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [600, 70000])
+def test_gradients_at_extreme_temperatures(dtype, V):
+    # Two rows each: logits a few temperatures apart, and one id ahead of all others by 0.5 at least, which
+    # a low temperature makes certain: whatever the others' factor is, their gradient is 0. Some ids are
+    # masked. Weights are such that every gradient fits its type, and at high temperatures large, since
+    # what lies below 1e-38 is not compared.
+    log(f"case logprob gradients at extreme temperatures {dtype} V={V}")
+    rng = np.random.default_rng(V)
+    temps = np.array([LEAST, 2e-38, 1e-37, 1e-35, 1e-30, B**-1 * 0.99, 1 / B, 1e-20, 1e20, B, B * 1.01, 1e30, 1e35, 1e37,
+                      2e38], np.float32)
+    T = np.repeat(temps, 2)
+    N, top = T.size, 3
+    x = np.empty((N, V), np.float32)
+    tokens = rng.integers(0, V - 9, N).astype(np.int32)
+    c = Case(rng, N, top, True)
+    for n in range(N):
+        t = float(T[n])
+        if n % 2 == 0:
+            z = rng.standard_normal(V) * min(3.0, 2e37 / t)
+            x[n] = t * z
+        else:
+            x[n] = -rng.uniform(0.5, 1.0, V)
+            x[n, tokens[n]] = 0.0
+        x[n, V - 9 :] = -np.inf
+        big = 1e6 if t > 1e19 else 1.0
+        c.a[n] = (8.0 if n % 2 else 1.5) * big
+        c.b[n] = 0.5 * big
+        c.u[n] = np.array([0.25, -0.25, 0.125]) * big
+    check_all(x, dtype, T, tokens, c, top)

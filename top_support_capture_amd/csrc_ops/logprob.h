@@ -319,15 +319,20 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
 
 // ---- the gradient ----------------------------------------------------------------------------------
 
-// dx_i = 2^t (alpha + beta t) with t = (x_i - m) c, plus `hit` at the token and u_j / T at the
-// alternatives.
+// dx_i = again (2^t (alpha + beta t) + hits) with t = (x_i - m) c; the hits are a / T at the token and
+// u_j / T at the alternatives, of this T. T again is the row's temperature, `again` a power of two: 1
+// from 2^-80 to 2^80. Past that the coefficients would leave float32, or lose digits, for temperatures
+// whose gradients do not (an element of numerator 0 would get 0 * inf). With again at most 2^40 the sums
+// stay below 2^127 for upstream gradients up to 2^32, and overflow only where the gradient itself does.
 struct LogprobCoef {
-  float m, c, alpha, beta;
+  float m, c, alpha, beta, T, again;
 };
 
 __device__ inline LogprobCoef logprob_coef(const LogprobRow& r, float T, float total, float b) {
-  const float g = 1.0f / (r.s * T);
-  return {r.m, plain_scale(T), (b == 0.0f ? -total : __builtin_fmaf(b, r.M, -total)) * g, -b * 0.69314718055994531f * g};
+  const float again = T < 0x1p-80f ? 0x1p40f : T > 0x1p80f ? 0x1p-40f : 1.0f;
+  const float scaled = T * again, g = 1.0f / (r.s * scaled);
+  return {r.m, plain_scale(T), (b == 0.0f ? -total : __builtin_fmaf(b, r.M, -total)) * g,
+          -b * 0.69314718055994531f * g, scaled, again};
 }
 
 template <int kE>
@@ -339,8 +344,16 @@ __device__ inline void logprob_grad_of(float (&x)[kE], const LogprobCoef& k) {
   }
 }
 
-// Writes the gradient of row[lo, hi), kU pieces in flight per thread. beside(at, x) adds what stands
-// beside the stream to the piece from `at` on.
+// The piece's gradient. beside(at, x) adds the hits among the elements from `at` on.
+template <int kE, class Beside>
+__device__ inline void logprob_grad_piece(float (&x)[kE], int64_t at, const LogprobCoef& k, Beside& beside) {
+  logprob_grad_of(x, k);
+  beside(at, x);
+#pragma unroll
+  for (int e = 0; e < kE; ++e) x[e] *= k.again;
+}
+
+// Writes the gradient of row[lo, hi), kU pieces in flight per thread.
 template <int DT, int kThr, int kU, class Beside>
 __device__ inline void logprob_grad_pass(const typename Row<DT>::Bits* row, typename Row<DT>::Bits* out, int64_t lo,
                                          int64_t hi, const LogprobCoef& k, Beside beside) {
@@ -356,16 +369,14 @@ __device__ inline void logprob_grad_pass(const typename Row<DT>::Bits* row, type
     for (int u = 0; u < kU; ++u) {
       float x[kE];
       v[u].unpack(x);
-      logprob_grad_of(x, k);
-      beside(at + u * kStep, x);
+      logprob_grad_piece(x, at + u * kStep, k, beside);
       Piece<DT>::store(out + at + u * kStep, x);
     }
   }
   for (; at < hi; at += kStep) {
     float x[kE];
     load_piece<DT>(row, at, hi, x);
-    logprob_grad_of(x, k);
-    beside(at, x);
+    logprob_grad_piece(x, at, k, beside);
     store_piece<DT>(out, at, hi, x);
   }
 }
@@ -420,14 +431,14 @@ __global__ void __launch_bounds__(kLogprobGradThreads, 8) logprob_grad_kernel(Lo
     __syncthreads();
   }
   const LogprobCoef k = logprob_coef(r, T, total, a.grad_entropy ? a.grad_entropy[n] : 0.0f);
-  const float hit = up / T;
+  const float hit = up / k.T;
   logprob_grad_pass<DT, kThr, kLogprobGradPieces>(row, out, lo, hi, k, [&](int64_t at, float(&x)[kE]) {
     if ((uint64_t)(token - at) < (unsigned)kE) add_at(x, (uint32_t)(token - at), hit);
     if constexpr (kTop) {
       const uint32_t chunk = (uint32_t)(at - lo) >> 3;
       if ((bits[chunk >> 5] >> (chunk & 31)) & 1u) {
         for (int j = 0; j < a.top; ++j)
-          if ((uint64_t)(ids[j] - at) < (unsigned)kE) add_at(x, (uint32_t)(ids[j] - at), ups[j] / T);
+          if ((uint64_t)(ids[j] - at) < (unsigned)kE) add_at(x, (uint32_t)(ids[j] - at), ups[j] / k.T);
       }
     }
   });
@@ -460,9 +471,10 @@ __global__ void __launch_bounds__(kThr, 8) logprob_fused_kernel(LogprobArgs a) {
     fill_zero<DT, kThr>(out, 0, a.V);
     return;
   }
-  const float up = a.grad_logprobs[n], hit = up / T;
+  const float up = a.grad_logprobs[n];
   const int64_t token = a.tokens[n];
   const LogprobCoef k = logprob_coef(r, T, up, a.grad_entropy ? a.grad_entropy[n] : 0.0f);
+  const float hit = up / k.T;
   auto beside = [&](int64_t at, float(&v)[kE]) {
     if ((uint64_t)(token - at) < (unsigned)kE) add_at(v, (uint32_t)(token - at), hit);
   };
@@ -472,8 +484,7 @@ __global__ void __launch_bounds__(kThr, 8) logprob_fused_kernel(LogprobArgs a) {
     float v[kE];
     Piece<DT>{held.at[i * kThr + threadIdx.x]}.unpack(v);
     const int64_t at = lo + (int64_t)threadIdx.x * kE;
-    logprob_grad_of(v, k);
-    beside(at, v);
+    logprob_grad_piece(v, at, k, beside);
     Piece<DT>::store(out + at, v);
   }
   logprob_grad_pass<DT, kThr, 4>(row, out, lo, a.V, k, beside);
