@@ -61,3 +61,34 @@ def test_gradients_at_extreme_temperatures(dtype, V):
         c.b[n] = 0.5 * big
         c.u[n] = np.array([0.25, -0.25, 0.125]) * big
     check_all(x, dtype, T, tokens, c, top)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [600, 70000])
+def test_logits_further_apart_than_their_type_reaches(dtype, V):
+    # From the lowest to the largest finite logit at temperatures that leave a few between them: a
+    # difference of two logits is past float32, and its exponent counts. (Temperatures up to 2.4e38, where 2 log2(e) / T is normal,
+    # so that the exponent's roundings are relative ones.) Below them, at any temperature, those that are
+    # so far behind have probability 0.
+    log(f"case logprobs of logits far apart {dtype} V={V}")
+    rng = np.random.default_rng(V + 1)
+    T = np.array([2.4e38, 1e38, 1e38, 3e37, 3e37, 1e36, 1.0, 1e-3], np.float32)
+    N, top = T.size, 5
+    far = torch.finfo(DT[dtype]).max
+    x = torch.from_numpy(rng.uniform(-1.0, 1.0, (N, V)) * far).to(DT[dtype]).float().numpy()
+    tokens = rng.integers(0, V, N).astype(np.int32)
+    for n in range(N):
+        x[n, rng.integers(0, V, V // 3)] = -far
+        x[n, int(rng.integers(0, V))] = far
+    x[2] = -far                                    # all but one at the lowest value
+    x[2, 7] = far
+    x[4, : V // 2] = -far                          # the maximum grows on the way
+    x[4, V // 2 :] = far
+    for n in (5, 6, 7):                            # one is ahead; its logprob fits float32
+        x[n] = -far
+        x[n, tokens[n]] = far
+    c = Case(rng, 5, top, True)
+    for w in (c.a, c.b, c.u):
+        w *= 1e5                                   # gradients above 1e-38, below which none is compared
+    check_all(x[:5], dtype, T[:5], tokens[:5], c, top)
+    check_all(x[5:], dtype, T[5:], tokens[5:], Case(rng, 3, 1, True), 1)

@@ -15,7 +15,7 @@ namespace tsc {
 
 constexpr int kTopThreads = 1024, kTopWaves = kTopThreads / kWaveSize;
 
-// State of a row or a part of it: the maximum, the sum of the numerators e = 2^t, t = (x - m) c,
+// State of a row or a part of it: the maximum, the sum of the numerators e = 2^t, t = (x - m) log2(e) / T,
 // and (kEnt) the sum of e t.
 struct LogprobPart {
   float m;
@@ -51,6 +51,18 @@ struct LogprobArgs {
 // Exponents below this have numerator 0; as a factor it keeps 0 * -inf out.
 constexpr float kLeastExponent = -200.0f;
 
+// The exponent t = (x - m) log2(e) / T as (half x - half m) c. From a temperature of 2^64 on half is 1/2,
+// so that the difference of any two finite logits stays finite: at 1e38 some that are 5e38 apart count.
+// Below, what is so far behind has numerator 0. Of a row, the same for the workgroup.
+struct ExponentScale {
+  float half, c;
+  __device__ inline float operator()(float x, float half_m) const { return __builtin_fmaf(x, half, -half_m) * c; }
+};
+constexpr float kFarFrom = 0x1p64f;
+__device__ inline ExponentScale exponent_scale(float T) {
+  return T >= kFarFrom ? ExponentScale{0.5f, plain_scale(0.5f * T)} : ExponentScale{1.0f, plain_scale(T)};
+}
+
 // A thread's running state: sums of up to 32 terms in float32, all else in float64. `at` is the
 // first piece (kTop only) that reached the maximum, -1 before the first one.
 template <bool kEnt, bool kTop>
@@ -58,9 +70,10 @@ struct LogprobState {
   float m = -__builtin_inff();
   int32_t at = -1;
   double s = 0.0, a = 0.0;
-  // kU pieces of kE elements, the first piece's index and the distance from one to the next.
-  template <int kU, int kE>
-  __device__ inline void add(const float (&x)[kU][kE], float c, int32_t piece, int32_t step) {
+  // kU pieces of kE elements, the first piece's index and the distance from one to the next. kFar: c.half
+  // is 1/2.
+  template <bool kFar, int kU, int kE>
+  __device__ inline void add(const float (&x)[kU][kE], ExponentScale c, int32_t piece, int32_t step) {
     float b = m;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -73,11 +86,12 @@ struct LogprobState {
       b = __builtin_fmaxf(b, most);
     }
     if constexpr (kTop) at = at < 0 ? piece : at;
-    const float base = b == -__builtin_inff() ? 0.0f : b;
+    const float base = b == -__builtin_inff() ? 0.0f : kFar ? 0.5f * b : b;
     float t4[4] = {}, a4[4] = {};
 #pragma unroll
     for (int i = 0; i < kU * kE; ++i) {
-      const float t = (x[i / kE][i % kE] - base) * c, e = __builtin_amdgcn_exp2f(t);
+      const float v = x[i / kE][i % kE], t = (kFar ? __builtin_fmaf(v, 0.5f, -base) : v - base) * c.c;
+      const float e = __builtin_amdgcn_exp2f(t);
       t4[i & 3] += e;
       if constexpr (kEnt) a4[i & 3] = __builtin_fmaf(e, __builtin_fmaxf(t, kLeastExponent), a4[i & 3]);
     }
@@ -85,11 +99,11 @@ struct LogprobState {
     s += (double)((t4[0] + t4[1]) + (t4[2] + t4[3]));
     if constexpr (kEnt) a += (double)((a4[0] + a4[1]) + (a4[2] + a4[3]));
   }
-  // Relative to M >= m; s and a of m = -inf are 0 (or NaN). With d = (m - M) c, e t becomes
+  // Relative to M >= m; s and a of m = -inf are 0 (or NaN). With d the exponent of m, e t becomes
   // 2^d e (t + d).
-  __device__ inline void rescale(float M, float c) {
+  __device__ inline void rescale(float M, ExponentScale c) {
     if (m == M) return;
-    const float d = (m - M) * c;
+    const float d = c(m, M * c.half);
     const double by = (double)__builtin_amdgcn_exp2f(d);
     if constexpr (kEnt) a = by * __builtin_fma((double)__builtin_fmaxf(d, kLeastExponent), s, a);
     s *= by;
@@ -105,7 +119,7 @@ struct LogprobShared {
 
 // The workgroup's state from its threads', the same for every thread.
 template <int kW, bool kEnt, bool kTop>
-__device__ inline LogprobPart block_part(LogprobState<kEnt, kTop> st, float c, LogprobShared<kW>& sh) {
+__device__ inline LogprobPart block_part(LogprobState<kEnt, kTop> st, ExponentScale c, LogprobShared<kW>& sh) {
   const uint32_t w = threadIdx.x / kWaveSize, lane = threadIdx.x & (kWaveSize - 1);
   st.rescale(wave_max(st.m), c);
   const double ws = wave_reduce(st.s, SumOp()), wa = kEnt ? wave_reduce(st.a, SumOp()) : 0.0;
@@ -134,10 +148,10 @@ struct NothingHeld {
 
 // A thread's state of row[lo, hi), lo a multiple of 8, in a workgroup of kThr threads. (32 float32
 // elements in flight per thread instead of 16 spill where alternatives are kept, and gain nothing.)
-template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce = false, class Held = NothingHeld>
-__device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
-                                                        float c, Held held = Held()) {
-  constexpr int kE = Piece<DT>::kSize, kU = 4;  // pieces in flight per thread
+template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce, bool kFar, int kU, class Held>
+__device__ inline LogprobState<kEnt, kTop> logprob_pass_of(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
+                                                           ExponentScale c, Held held) {
+  constexpr int kE = Piece<DT>::kSize;  // kU of them in flight per thread
   constexpr int64_t kStep = kThr * kE;
   LogprobState<kEnt, kTop> st;
   int64_t at = lo + (int64_t)threadIdx.x * kE;
@@ -166,10 +180,20 @@ __device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::
       for (int u = 0; u < kU; ++u)
         if (at + u * kStep < hi && at + u * kStep + kE > hi) load_part<DT>(row, at + u * kStep, hi, x[u]);
     }
-    st.add(x, c, (int32_t)(at / kE), (int32_t)(kStep / kE));
+    st.template add<kFar>(x, c, (int32_t)(at / kE), (int32_t)(kStep / kE));
   }
   if (lo + (int64_t)threadIdx.x * kE >= hi) st.at = -1;  // nothing of the row
   return st;
+}
+
+// Logits that may be far apart take another way, so that the usual one keeps a subtraction and its
+// registers; with one piece in flight it spills nothing.
+template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce = false, class Held = NothingHeld>
+__device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
+                                                        ExponentScale c, Held held = Held()) {
+  if (__builtin_amdgcn_readfirstlane(c.half == 1.0f))
+    return logprob_pass_of<DT, kThr, kEnt, kTop, kOnce, false, 4>(row, lo, hi, c, held);
+  return logprob_pass_of<DT, kThr, kEnt, kTop, kOnce, true, 1>(row, lo, hi, c, held);
 }
 
 template <bool kEnt>
@@ -245,7 +269,7 @@ __global__ void __launch_bounds__(kThr, 8) logprob_kernel(LogprobArgs a) {
   uint64_t key = 0;
   if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get(row + a.tokens[n]);
-    const float c = plain_scale(a.T(n));
+    const ExponentScale c = exponent_scale(a.T(n));
     const auto st = logprob_pass<DT, kThr, kEnt, kTop, kOnce>(row, 0, a.V, c);
     if constexpr (kTop) key = state_key(st);
     p = block_part<kThr / kWaveSize>(st, c, sh);
@@ -273,7 +297,7 @@ __global__ void __launch_bounds__(kTopThreads, 8) logprob_slice_kernel(LogprobAr
   const int64_t item = blockIdx.x, n = item / a.slices, sl = item - n * a.slices;
   const int64_t lo = sl * a.slice_len, hi = lo + a.slice_len < a.V ? lo + a.slice_len : a.V;
   const auto* row = (const typename Row<DT>::Bits*)a.logits + n * a.ld;
-  const float c = plain_scale(a.T(n));
+  const ExponentScale c = exponent_scale(a.T(n));
   const auto st = logprob_pass<DT, kTopThreads, kEnt, kTop>(row, lo, hi, c);
   if (logprob_early_status(a, n) != TSC_ROW_OK) return;  // not looked at earlier: the row is on its way by now
   const LogprobPart p = block_part<kTopWaves>(st, c, sh);
@@ -296,7 +320,7 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
   float x = 0.0f;
   if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get((const typename Row<DT>::Bits*)a.logits + n * a.ld + a.tokens[n]);
-    const float c = plain_scale(a.T(n));
+    const ExponentScale c = exponent_scale(a.T(n));
     LogprobState<kEnt, kTop> st;
     if (lane < a.slices) {
       const LogprobPart q = a.parts[n * a.slices + lane];
@@ -319,19 +343,22 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
 
 // ---- the gradient ----------------------------------------------------------------------------------
 
-// dx_i = again (2^t (alpha + beta t) + hits) with t = (x_i - m) c; the hits are a / T at the token and
+// dx_i = again (2^t (alpha + beta t) + hits) with t the exponent of x_i; the hits are a / T at the token and
 // u_j / T at the alternatives, of this T. T again is the row's temperature, `again` a power of two: 1
 // from 2^-80 to 2^80. Past that the coefficients would leave float32, or lose digits, for temperatures
 // whose gradients do not (an element of numerator 0 would get 0 * inf). With again at most 2^40 the sums
 // stay below 2^127 for upstream gradients up to 2^32, and overflow only where the gradient itself does.
 struct LogprobCoef {
-  float m, c, alpha, beta, T, again;
+  float half_m;
+  ExponentScale c;
+  float alpha, beta, T, again;
 };
 
 __device__ inline LogprobCoef logprob_coef(const LogprobRow& r, float T, float total, float b) {
   const float again = T < 0x1p-80f ? 0x1p40f : T > 0x1p80f ? 0x1p-40f : 1.0f;
   const float scaled = T * again, g = 1.0f / (r.s * scaled);
-  return {r.m, plain_scale(T), (b == 0.0f ? -total : __builtin_fmaf(b, r.M, -total)) * g,
+  const ExponentScale c = exponent_scale(T);
+  return {r.m * c.half, c, (b == 0.0f ? -total : __builtin_fmaf(b, r.M, -total)) * g,
           -b * 0.69314718055994531f * g, scaled, again};
 }
 
@@ -339,7 +366,7 @@ template <int kE>
 __device__ inline void logprob_grad_of(float (&x)[kE], const LogprobCoef& k) {
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
-    const float t = __builtin_fmaxf((x[e] - k.m) * k.c, kLeastExponent);
+    const float t = __builtin_fmaxf(k.c(x[e], k.half_m), kLeastExponent);
     x[e] = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(k.beta, t, k.alpha);
   }
 }
@@ -461,7 +488,8 @@ __global__ void __launch_bounds__(kThr, 8) logprob_fused_kernel(LogprobArgs a) {
   const B* row = (const B*)a.logits + n * a.ld;
   B* out = (B*)a.grad + n * a.V;
   float x = 0.0f;
-  const float T = a.T(n), c = plain_scale(T);
+  const float T = a.T(n);
+  const ExponentScale c = exponent_scale(T);
   if (early == TSC_ROW_OK) {
     if (threadIdx.x == 0) x = Row<DT>::get(row + a.tokens[n]);
     p = block_part<kThr / kWaveSize>(logprob_pass<DT, kThr, kEnt, false>(row, 0, a.V, c, held), c, sh);
