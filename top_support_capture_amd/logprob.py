@@ -7,6 +7,7 @@ pass runs on the stream that the forward ran on, allocates the gradient, and syn
 """
 from __future__ import annotations
 
+import warnings
 from functools import lru_cache
 from typing import NamedTuple, Optional
 
@@ -163,7 +164,8 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, grad_logprob
                         stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobsGradOutput:
     """The values of ``token_logprobs`` and the gradient of sum(grad_logprobs * logprobs) +
     sum(grad_entropy * entropy) with respect to ``logits``, in one call and without autograd.
-    ``grad_logprobs`` and, if given, ``grad_entropy``: float32 [N]."""
+    ``grad_logprobs`` and, if given, ``grad_entropy``: float32 [N]. They are taken as constants (with a
+    warning if they ask for a gradient that would not reach them)."""
     if forward_ad._current_level >= 0:
         _refuse_tangents("token_logprobs_grad", logits, temperature, grad_logprobs, grad_entropy)
     lib = library()
@@ -171,6 +173,10 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, grad_logprob
     _check(grad_logprobs, "grad_logprobs", torch.float32, N, dev)
     if grad_entropy is not None:
         _check(grad_entropy, "grad_entropy", torch.float32, N, dev)
+    if torch.is_grad_enabled() and (grad_logprobs.requires_grad
+                                    or (grad_entropy is not None and grad_entropy.requires_grad)):
+        warnings.warn("token_logprobs_grad takes grad_logprobs and grad_entropy as constants: no gradient "
+                      "reaches them (detach them to say so)", stacklevel=2)
     nbytes = _grad_workspace(N, V)
 
     def go(s):
