@@ -24,7 +24,7 @@ def test_weights_that_ask_for_gradients_are_warned_of(launches, which):
         x, tok = torch.zeros(2, 8, **d), torch.zeros(2, dtype=torch.int32, **d)
         kw = dict(grad_logprobs=torch.ones(2, **d), grad_entropy=torch.ones(2, **d))
         with warnings.catch_warnings():
-            warnings.simplefilter("error")
+            warnings.filterwarnings("error", message=".*constants")
             tsc.token_logprobs_grad(x.clone().requires_grad_(), tok, **kw)  # logits of a model: as ever
             kw[which].requires_grad_()
             with torch.no_grad():
