@@ -34,7 +34,7 @@ class TokenLogprobsOutput(NamedTuple):
 
 class TokenLogprobsGradOutput(NamedTuple):
     logprobs: torch.Tensor           # float32 [N]
-    entropy: Optional[torch.Tensor]  # float32 [N] (None without grad_entropy)
+    entropy: Optional[torch.Tensor]  # float32 [N] (None unless requested, or weighted by grad_entropy)
     grad_logits: torch.Tensor        # [N, V], the logits' dtype
     row_status: torch.Tensor         # int8 [N]
 
@@ -161,9 +161,11 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Opti
 def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, grad_logprobs: torch.Tensor,
                         temperature: Optional[torch.Tensor] = None,
                         grad_entropy: Optional[torch.Tensor] = None,
-                        stream: Optional[torch.cuda.Stream] = None) -> TokenLogprobsGradOutput:
+                        stream: Optional[torch.cuda.Stream] = None,
+                        return_entropy: bool = False) -> TokenLogprobsGradOutput:
     """The values of ``token_logprobs`` and the gradient of sum(grad_logprobs * logprobs) +
-    sum(grad_entropy * entropy) with respect to ``logits``, in one call and without autograd.
+    sum(grad_entropy * entropy) with respect to ``logits``, in one call and without autograd. The entropy
+    is given with ``grad_entropy``, or alone with ``return_entropy``.
     ``grad_logprobs`` and, if given, ``grad_entropy``: float32 [N]. They are taken as constants (with a
     warning if they ask for a gradient that would not reach them)."""
     if forward_ad._current_level >= 0:
@@ -182,7 +184,7 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, grad_logprob
     def go(s):
         f32 = dict(dtype=torch.float32, device=dev)
         out = TokenLogprobsGradOutput(torch.empty(N, **f32),
-                                      None if grad_entropy is None else torch.empty(N, **f32),
+                                      torch.empty(N, **f32) if return_entropy or grad_entropy is not None else None,
                                       torch.empty((N, V), dtype=logits.dtype, device=dev),
                                       torch.empty(N, dtype=torch.int8, device=dev))
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
