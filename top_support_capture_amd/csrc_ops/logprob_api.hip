@@ -138,9 +138,15 @@ hipError_t launch_grad(tsc::LogprobArgs& a, int32_t dtype, hipStream_t s) {
 // short; one launch instead of two or three.
 bool fused(int64_t N, int64_t V) { return N >= 128 || V <= 65536; }
 
-// A second reading of a row comes from the last-level cache if the rows of all resident workgroups
-// fit there, beside the gradients on their way out.
-constexpr int64_t kCached = kCacheBytes * 7 / 10;
+// Small workgroups where the rows of all of them that are resident (2048) stay in this part of the
+// last-level cache for their second reading, beside the gradients on their way out. Small against large,
+// us, with the entropy, by those rows' MB: bf16, 1024 rows, 94 MB 29 against 34, 125 MB 34 / 37, 156 MB
+// 40 / 45, 172 MB 50 / 48, 352 MB 93 / 85; 4096 rows, 94 MB 89 / 108, 156 MB 146 / 164, 172 MB 166 / 171.
+// float32 rows of as many bytes have half the elements, and the ends that small workgroups overlap weigh
+// less: 1024 rows, 94 MB 22 / 28, 125 MB 30 / 33, 141 MB 38 / 35; 4096 rows, 94 MB 83 / 82, 109 MB 101 / 92,
+// 156 MB 140 / 125.
+template <int DT>
+constexpr int64_t kCached = kCacheBytes * (DT == TSC_DTYPE_F32 ? 4 : 7) / 10;
 
 // LDS that holds the first pieces of a workgroup's row for the second reading, as much as leaves room
 // for two large workgroups, or eight small ones, on a CU.
@@ -159,8 +165,8 @@ hipError_t launch_fused(tsc::LogprobArgs a, hipStream_t s) {
 template <int DT, bool kEnt>
 hipError_t launch_fused(const tsc::LogprobArgs& a, hipStream_t s) {
   const int64_t rows = 2048 * a.V * (DT == TSC_DTYPE_F32 ? 4 : 2);  // of 8 workgroups on each CU
-  return a.N >= kManyRows && rows <= kCached ? launch_fused<DT, kSmall, kEnt>(a, s)
-                                             : launch_fused<DT, tsc::kTopThreads, kEnt>(a, s);
+  return a.N >= kManyRows && rows <= kCached<DT> ? launch_fused<DT, kSmall, kEnt>(a, s)
+                                                 : launch_fused<DT, tsc::kTopThreads, kEnt>(a, s);
 }
 
 hipError_t launch_fused(const tsc::LogprobArgs& a, int32_t dtype, bool entropy, hipStream_t s) {
