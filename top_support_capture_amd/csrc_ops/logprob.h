@@ -60,7 +60,8 @@ struct ExponentScale {
 };
 constexpr float kFarFrom = 0x1p64f;
 __device__ inline ExponentScale exponent_scale(float T) {
-  return T >= kFarFrom ? ExponentScale{0.5f, plain_scale(0.5f * T)} : ExponentScale{1.0f, plain_scale(T)};
+  const float half = T >= kFarFrom ? 0.5f : 1.0f;
+  return {half, plain_scale(half * T)};  // one division
 }
 
 // A thread's running state: sums of up to 32 terms in float32, all else in float64. `at` is the
@@ -186,14 +187,22 @@ __device__ inline LogprobState<kEnt, kTop> logprob_pass_of(const typename Row<DT
   return st;
 }
 
-// Logits that may be far apart take another way, so that the usual one keeps a subtraction and its
-// registers; with one piece in flight it spills nothing.
+// Rows whose logits may be far apart are passed over again, by a function that is called: so the usual loop
+// keeps a subtraction and its registers, and its loads do not wait for the temperature. (With both ways in
+// the loop 256 rows of 151936 with 5 alternatives take 49 us instead of 24.2, with this one inlined 25.4.)
+template <int DT, int kThr, bool kEnt, bool kTop, class Held>
+__device__ __attribute__((noinline)) LogprobState<kEnt, kTop> logprob_far_pass(const typename Row<DT>::Bits* row,
+                                                                               int64_t lo, int64_t hi, ExponentScale c,
+                                                                               Held held) {
+  return logprob_pass_of<DT, kThr, kEnt, kTop, false, true, 1>(row, lo, hi, c, held);
+}
 template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce = false, class Held = NothingHeld>
 __device__ inline LogprobState<kEnt, kTop> logprob_pass(const typename Row<DT>::Bits* row, int64_t lo, int64_t hi,
                                                         ExponentScale c, Held held = Held()) {
-  if (__builtin_amdgcn_readfirstlane(c.half == 1.0f))
-    return logprob_pass_of<DT, kThr, kEnt, kTop, kOnce, false, 4>(row, lo, hi, c, held);
-  return logprob_pass_of<DT, kThr, kEnt, kTop, kOnce, true, 1>(row, lo, hi, c, held);
+  auto st = logprob_pass_of<DT, kThr, kEnt, kTop, kOnce, false, 4>(row, lo, hi, c, held);
+  if (__builtin_expect(__builtin_amdgcn_readfirstlane(c.half != 1.0f), 0))
+    st = logprob_far_pass<DT, kThr, kEnt, kTop>(row, lo, hi, c, held);
+  return st;
 }
 
 template <bool kEnt>
