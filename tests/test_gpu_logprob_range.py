@@ -32,7 +32,7 @@ def check_all(x, dtype, T, tokens, c, top):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("V", [600, 70000])
+@pytest.mark.parametrize("V", [600, 60000, 70000])
 def test_gradients_at_extreme_temperatures(dtype, V):
     # Two rows each: logits a few temperatures apart, and one id ahead of all others by 0.5 at least, which
     # a low temperature makes certain: whatever the others' factor is, their gradient is 0. Some ids are
@@ -64,7 +64,7 @@ def test_gradients_at_extreme_temperatures(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("V", [600, 70000])
+@pytest.mark.parametrize("V", [600, 60000, 70000])
 def test_logits_further_apart_than_their_type_reaches(dtype, V):
     # From the lowest to the largest finite logit at temperatures that leave a few between them: a
     # difference of two logits is past float32, and its exponent counts. (Temperatures up to 2.4e38, where 2 log2(e) / T is normal,
@@ -92,3 +92,38 @@ def test_logits_further_apart_than_their_type_reaches(dtype, V):
         w *= 1e5                                   # gradients above 1e-38, below which none is compared
     check_all(x[:5], dtype, T[:5], tokens[:5], c, top)
     check_all(x[5:], dtype, T[5:], tokens[5:], Case(rng, 3, 1, True), 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("top", [0, 4])
+def test_logits_far_apart_in_many_rows(dtype, top):
+    # The same, in the workgroups of batches of 128 and of 1024 rows: the rows of a smaller batch over and over.
+    log(f"case logprobs of many rows of logits far apart {dtype} top={top}")
+    rng = np.random.default_rng(top)
+    V, k = 9001, 6
+    T = np.array([2e38, 1e38, 5e37, 2.0**64, 2.0**63, 0.5], np.float32)
+    far = torch.finfo(DT[dtype]).max
+    xt = torch.from_numpy(rng.uniform(-1.0, 1.0, (k, V)) * np.minimum(4 * T[:, None].astype(np.float64), far)).to(DT[dtype])
+    x, tokens = xt.double().numpy(), rng.integers(0, V, k).astype(np.int32)
+    c = Case(rng, k, top, True)
+    for w in (c.a, c.b) + ((c.u,) if top else ()):
+        w[:3] *= 1e5
+    for N in (128, 1024):
+        every = np.arange(N) % k
+        tk, tt = tensor(tokens[every], torch.int32), tensor(T[every], torch.float32)
+        leaf = xt.to(DEV)[torch.from_numpy(every).to(DEV)].requires_grad_()
+        many = Case(rng, 1, top, True)
+        many.a, many.b, many.u = (None if w is None else w[every] for w in (c.a, c.b, c.u))
+        out = tsc.token_logprobs(leaf, tk, tt, top=top, return_entropy=True)
+        cut = lambda o: o._replace(**{f: v[:k] for f, v in o._asdict().items() if v is not None})
+        rows = check_values(x, T, tokens, top, cut(out))
+        grad = backward(leaf, out, many)
+        check_grad(x, dtype, T, tokens, rows, c, grad[:k])
+        one = tsc.token_logprobs_grad(leaf.detach(), tk, tensor(many.a, torch.float32), tt,
+                                      grad_entropy=tensor(many.b, torch.float32))
+        check_values(x, T, tokens, 0, cut(one))
+        few = Case(rng, k, 0, True)
+        few.a, few.b = c.a, c.b
+        check_grad(x, dtype, T, tokens, rows, few, one.grad_logits[:k])
+        for v in (out.logprobs.detach(), out.entropy.detach(), grad, one.logprobs, one.grad_logits):
+            assert torch.equal(v, v[torch.from_numpy(every).to(DEV)])
