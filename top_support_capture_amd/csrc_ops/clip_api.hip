@@ -133,8 +133,8 @@ int64_t launch_in_place(const Lists& l, int64_t from, const tsc::ClipNorm& c, hi
 
 void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
   // Tensors of one type whose results lie as they do themselves, as in two flat buffers, need no
-  // addresses for the results: more tensors to a launch (224 of 24 MB in all take one, 11 us, instead of
-  // two, 10 and 5).
+  // addresses for the results: more tensors to a launch (224 of 24 MB in all take one, 11.1 us, instead of
+  // two, 13.2).
   bool own = true, narrow = true, flat = true;
   uint64_t distance = 0;
   int64_t first = -1;
@@ -159,7 +159,7 @@ void launch_scale(const Lists& l, tsc::ClipNorm c, hipStream_t s) {
 }
 
 // Whether every workgroup of the scaling may add up the partial sums by itself, which saves a
-// launch: few of either.
+// launch: few of either, in the smallest units that a scaling takes.
 bool joins_inline(const Lists& l, int64_t partials) {
   int64_t units = 0;
   for (int64_t i = 0; i < l.count; ++i) units += ceil_div(l.numels[i], 2048);

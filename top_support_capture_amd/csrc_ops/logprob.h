@@ -260,11 +260,12 @@ __device__ inline LogprobRow logprob_finish(const LogprobArgs& a, int64_t n, int
   return {p.m, (float)p.s, (float)M, ok};
 }
 
-// A row per workgroup, read once. kOnce: nontemporally. 4096 rows of 151936 bfloat16 logits take 192 us,
-// 6.5 TB/s, with the first alternative 199; 1024 of them with the entropy 57 us, 5.5 TB/s. What keeps
-// the latter from a bare read's rate are its vector instructions: 8 an element, of which the exponential
-// takes four times as long, fill about two thirds of the time. 256 rows, one to a CU: 16.4 us, 18 with the
-// entropy, which has too few waves a CU to hide the first and the last steps' latency.
+// A row per workgroup, read once. kOnce: nontemporally. 4096 rows of 151936 bfloat16 logits take 194 us,
+// 6.4 TB/s, with the first alternative 194 to 204; 1024 of them with the entropy 58 us, 5.4 TB/s, and 66 in
+// front of a backward pass, where they are not read nontemporally. What keeps it from a bare read's rate
+// are its vector instructions: 8 an element, of which the exponential takes four times as long, fill about
+// two thirds of the time. 256 rows, one to a CU: 18.8 us from memory (17.0 from the last-level cache), with
+// the entropy 20.2 (18.2), which has too few waves a CU to hide the first and the last steps' latency.
 template <int DT, int kThr, bool kEnt, bool kTop, bool kOnce>
 __global__ void __launch_bounds__(kThr, 8) logprob_kernel(LogprobArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint64_t dyn_top[];
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThr, 8) logprob_kernel(LogprobArgs a) {
 }
 
 // Few rows: a slice of a row per workgroup, then the rows from their slices. One row of 151936 bfloat16
-// logits 7.1 us for both, 13.6 with 20 alternatives: two launches' latency and the selection's steps. (Joins
+// logits 7.0 us for both, 13.3 with 20 alternatives: two launches' latency and the selection's steps. (Joins
 // by 256 threads instead of 1024 take 6.0 us against 5.0 with 20 alternatives, 16 against 7.6 with 128.)
 template <int DT, bool kEnt, bool kTop>
 __global__ void __launch_bounds__(kTopThreads, 8) logprob_slice_kernel(LogprobArgs a) {
@@ -427,7 +428,8 @@ __device__ inline void add_at(float (&x)[kE], uint32_t i, float v) {
 constexpr int kLogprobGradThreads = 256, kLogprobGradPieces = 4;  // in flight per thread
 constexpr int64_t kLogprobGradSegment = 8192;  // elements, or more to bound the grid
 
-// A segment of a row per workgroup: 83 us for 1024 rows of 151936 bfloat16 logits, 7.1 TB/s behind the L2.
+// A segment of a row per workgroup: 83 us for 1024 rows of 151936 bfloat16 logits, a tenth of them padding,
+// 7.1 TB/s behind the L2; 93 us without padding.
 // (Segments of 16384 elements 88, of 4096 with two pieces in flight 92; reversing the rows' order, so
 // that those read last come first, 84.) Pieces that the entries of a list join are looked for, so that
 // each result is rounded and written once. With alternatives (kTop), a bit for each 8 elements of the segment
@@ -482,7 +484,8 @@ __global__ void __launch_bounds__(kLogprobGradThreads, 8) logprob_grad_kernel(Lo
 
 // Values and gradient, a row per workgroup: the second reading of the row comes from LDS as far as
 // that goes, and from the last-level cache while the rows in flight fit there. 512 rows of 262144
-// bfloat16 logits 122 us, 724 MB behind the L2 at 5.9 TB/s; without the LDS 126. (With it, one workgroup to
+// bfloat16 logits, a twentieth of them padding, 120 to 128 us, 724 MB behind the L2 at 5.7 to 6.0 TB/s; in one
+// run 122, and without the LDS 126. (With it, one workgroup to
 // a CU no longer pays where the rows exceed the cache: 1024 such rows 270 us, in pairs 253.)
 template <int DT, int kThr, bool kEnt>
 __global__ void __launch_bounds__(kThr, 8) logprob_fused_kernel(LogprobArgs a) {

@@ -12,12 +12,25 @@ namespace {
 static_assert(TSC_MAX_TOP == tsc::kTopMost, "the selection's lists hold that many");
 
 // Whole rows for a workgroup each when there are rows enough, or short ones; slices otherwise, as
-// many as the chip holds at once (two workgroups on each CU), of 8192 elements at least, and whole
-// steps of a workgroup for either type. Slices cost a second launch, and with alternatives a second
-// selection. Sliced against whole, us, without / with 5 alternatives and the entropy: bf16 of 151936, 1
-// row 7.1 / 13.6 against 11.5 / 18.4, 64 rows 11.4 / 20.3 against 13.1 / 20.2, 128 rows 15.8 / 24.8
-// against 13.6 / 20.9; float32 of 129280, 100 rows 15.1 / 23.2 against 13.6 / 19.9, of 262144, 64 rows
-// 16.1 / 23.4 against 20.8 / 30.1; bf16 of 65536, 16 rows 7.5 / 13.7 against 6.7 / 11.7.
+// many as the chip holds at once (two workgroups on each CU), of 8192 elements at least, in multiples of
+// 4096 (a step of a workgroup for float32, half of one for bfloat16). Slices cost a second launch, and with
+// alternatives a second selection. The borders count elements, not bytes: a row alone in a workgroup takes
+// nearly as long in either type. Sliced against whole, us a call in a captured graph, without alternatives,
+// then with 5 and the entropy:
+//   bf16  65536   1 row   6.8 /  6.4, 13.0 / 11.7    64 rows 11.5 /  7.7, 20.1 / 12.6
+//        100000  16 rows  8.1 / 10.6, 14.7 / 17.0    64 rows 11.8 / 11.8, 20.6 / 18.3   127 rows 13.2 / 12.4, 21.8 / 18.8
+//        151936   1 row   6.8 / 11.9, 13.4 / 18.8    64 rows 12.1 / 14.4, 21.4 / 21.6   127 rows 16.7 / 15.7, 26.2 / 22.1
+//        200000  16 rows 10.8 / 16.0, 20.0 / 24.2    64 rows 13.2 / 17.7, 22.0 / 26.2   127 rows 18.2 / 19.7, 26.9 / 26.8
+//        262144  16 rows 11.2 / 19.1, 20.6 / 27.6    64 rows 13.0 / 20.0, 21.6 / 28.7   127 rows 18.9 / 21.9, 27.2 / 29.4
+//   f32   65536   1 row   6.1 /  7.2, 11.9 / 12.5    64 rows 10.2 /  9.5, 18.6 / 14.6
+//        100000  16 rows  7.7 / 10.9, 13.8 / 17.1    64 rows 11.2 / 13.3, 19.5 / 18.9   127 rows 16.6 / 15.3, 24.6 / 19.9
+//        129280  16 rows  8.1 / 14.2, 14.2 / 20.5   100 rows 17.0 / 16.6, 24.9 / 21.9   127 rows 18.1 / 17.8, 25.5 / 22.1
+//        151936  16 rows  9.6 / 16.3, 18.3 / 23.1    64 rows 14.9 / 17.3, 23.2 / 23.7   127 rows 20.4 / 20.1, 28.5 / 24.7
+//        200000  16 rows 10.2 / 19.7, 19.2 / 27.3    64 rows 17.0 / 21.5, 25.0 / 28.4   127 rows 25.4 / 26.1, 33.6 / 29.5
+//        262144  16 rows 10.0 / 23.0, 19.2 / 31.8    64 rows 18.2 / 25.5, 25.6 / 33.0   127 rows 29.6 / 31.9, 37.2 / 34.3
+// With 160 rows whole ones are faster throughout (bf16 262144 24.0 / 21.8, 33.0 / 29.7). With alternatives
+// the border of 160000 lies between 151936, where 64 rows are even, and 200000, where slices win by 4 us;
+// more than 100 rows of those would gain up to 4 us whole, and 32 rows of 100000 2.5.
 Cut pass_cut(int64_t N, int64_t V, int32_t top) {
   if (N >= 128 || V <= 65536 || (top > 0 && N >= 64 && V <= 160000)) return {1, V};
   const int64_t most = ceil_div(V, 8192) < tsc::kMaxSlices ? ceil_div(V, 8192) : tsc::kMaxSlices;
@@ -35,9 +48,9 @@ Cut segment_cut(int64_t N, int64_t V) {
 constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
 
 // With this many rows a smaller workgroup reads one, so that the ends of some overlap the loads of
-// others. (With entropies, bf16: 4096 rows of 2000 take 18 us against 54, of 32000 55 against 68, 1024
-// rows of 151936 61 against 64; but 256 rows of those 28 against 20. With 5 alternatives 512 threads:
-// 4096 rows of 32000 73 us against 97, of 2000 44 against 81; with 20, of 151936 261 against 271 and, with
+// others. (With entropies, bf16: 4096 rows of 2000 take 18 us against 53, of 32000 57 against 69, 1024
+// rows of 151936 59.5 against 59.9; but 256 rows of those 31 against 22. With 5 alternatives 512 threads:
+// 4096 rows of 32000 74 us against 98, of 2000 45 against 83; with 20, of 151936 262 against 262 and, with
 // 256 threads, 287.)
 constexpr int64_t kManyRows = 1024;
 constexpr int kSmall = 256, kSmallTop = 512;

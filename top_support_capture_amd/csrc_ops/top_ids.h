@@ -8,7 +8,7 @@
 // compared with the bound; what reaches it is ranked.
 //
 // All of it is a chain of short steps between barriers. For 256 rows of 151936 bfloat16 logits it adds
-// 3.6 us to a pass of 16.4 for one alternative, 4 for 20, 8 for 64 and 14 for 128 (waves' best, ranks
+// 4.4 us to a pass of 18.8 for one alternative, 5.5 for 20, 8.2 for 64 and 13.5 for 128 (waves' best, ranks
 // and pieces all grow with n); with rows enough other workgroups' loads cover most of it.
 #pragma once
 
