@@ -56,7 +56,7 @@ size_t tsc_token_logprobs_workspace(int64_t N, int64_t V, int32_t top);
  *     grad_logits[n, i] = ( a [i = t] + sum_j u_j [i = id_j] - p_i (a + sum_j u_j)
  *                           - b p_i (ln p_i + entropy[n]) ) / temperature[n]
  * and 0 in rows that are not TSC_ROW_OK. For every temperature that a row may have and upstream
- * gradients up to 2^32 in size (|b|, and |a| and the |u_j| together), no step on the way leaves float32:
+ * gradients up to 2^20 in size (|b|, and |a| and the |u_j| together), no step on the way leaves float32:
  * an element is infinite only where its gradient lies past its type, and 0 where p_i vanishes.
  * grad_logprobs, grad_entropy [N], grad_top [N, top] float32, each may be NULL (0). grad_entropy
  *              asks for `stats` of a call that gave the entropy. With grad_top, top_ids is read.

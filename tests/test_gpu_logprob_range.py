@@ -64,6 +64,24 @@ def test_gradients_at_extreme_temperatures(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [600, 70000])
+def test_large_weights_at_low_temperatures(dtype, V):
+    # The largest upstream gradients that the header names, where p is 1 at the token and 0 elsewhere: a / T
+    # and p a / T are past float32, and cancel.
+    log(f"case logprob gradients of large weights {dtype} V={V}")
+    rng = np.random.default_rng(V + 2)
+    T = np.array([LEAST, 2e-38, 1e-36, 1e-30, 1 / B, 1e-20], np.float32)
+    N = T.size
+    x = -rng.uniform(0.5, 1.0, (N, V)).astype(np.float32)
+    tokens = rng.integers(0, V, N).astype(np.int32)
+    x[np.arange(N), tokens] = 0.0
+    x[:, :: 7] = np.where(x[:, :: 7] < 0, -np.inf, 0.0)
+    c = Case(rng, N, 1, True)
+    c.a[:], c.b[:], c.u[:] = 2.0**20, -(2.0**20), 0.0
+    check_all(x, dtype, T, tokens, c, 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [600, 60000, 70000])
 def test_logits_further_apart_than_their_type_reaches(dtype, V):
     # From the lowest to the largest finite logit at temperatures that leave a few between them: a

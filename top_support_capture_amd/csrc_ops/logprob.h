@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kTop ? kTopThreads : kWaveSize) logprob_join_k
 // u_j / T at the alternatives, of this T. T again is the row's temperature, `again` a power of two: 1
 // from 2^-80 to 2^80. Past that the coefficients would leave float32, or lose digits, for temperatures
 // whose gradients do not (an element of numerator 0 would get 0 * inf). With again at most 2^40 the sums
-// stay below 2^127 for upstream gradients up to 2^32, and overflow only where the gradient itself does.
+// stay below 2^127 for upstream gradients up to 2^32; up to 2^20 what the roundings of a hit and of the
+// stream leave where they cancel, 2^-22 of the hit, is finite too.
 struct LogprobCoef {
   float half_m;
   ExponentScale c;
